@@ -69,8 +69,11 @@ enum {
   MD_DEV_BAD_TOKEN = 4,    /* a token id outside [0, V) reached tree_accept or   */
                            /* a Hydra head input                                */
   MD_DEV_TIMEOUT = 8,      /* a pipeline wait exceeded its bound                 */
-  MD_DEV_BAD_PATH = 16     /* md_tree_commit got a length or path that is not a  */
+  MD_DEV_BAD_PATH = 16,    /* md_tree_commit got a length or path that is not a  */
                            /* root-to-node path of the tree                       */
+  MD_DEV_BAD_PAGE = 32,    /* a block table entry outside the pool, a page nobody */
+                           /* holds given back, or an impossible page count       */
+  MD_DEV_NO_PAGES = 64     /* the pool has too few free pages for a resize or fork */
 };
 
 /* Supported ranges (anything else: MD_ERR_UNSUPPORTED).
@@ -81,6 +84,8 @@ enum {
  *              h and b1 must be 16-byte aligned).
  *   tree:      1 <= T <= 128, depth <= K.
  *   attention: dh in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 16.
+ *   paged:     as attention; page_size % 16 == 0 for md_tree_attention_paged,
+ *              any page_size >= 1 for the other calls; B <= 65535.
  */
 #define MD_MAX_T 128
 #define MD_MAX_K 8
@@ -485,6 +490,149 @@ MD_API md_status md_tree_commit(md_bf16* k_cache, md_bf16* v_cache, int32_t S_ma
                                 const int32_t* accept_len, const int32_t* path, int32_t K, const int32_t* bonus,
                                 int32_t* new_prefix_len, int32_t* next_root, int32_t* next_head_row,
                                 void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* 6. The step over a paged KV cache.                                        */
+/* ------------------------------------------------------------------------ */
+
+/* A server keeps the KV cache of its requests in pages of page_size slots:
+ *
+ *   k_pages, v_pages  [pool_pages, Hkv, page_size, dh] bf16 for one layer
+ *                     (the calls that work on every layer take
+ *                     [layers, pool_pages, Hkv, page_size, dh]);
+ *   block_table       [B, max_pages] int32: slot s of request b is row
+ *                     s % page_size of page block_table[b, s / page_size].
+ *
+ * A contiguous cache [B, Hkv, S_max, dh] is the case of one page a request:
+ * page_size = S_max, block_table[b, 0] = b. Pages of whole prefixes may be
+ * shared by requests; the slots from prefix_len[b] on, which these calls write,
+ * must lie in pages that request b alone holds (md_pages_fork keeps it so).
+ * What a page holds in slots that no request uses does not matter, NaN included.
+ *
+ * In every call prefix_len[b] = -1 marks an idle slot of a padded batch: its
+ * attention output is zero, the other outputs are as each call says, nothing is
+ * read or written through its row of the table, and no status bit is set. A
+ * page id outside [0, pool_pages) where one is needed sets MD_DEV_BAD_PAGE. */
+
+/* Output types of md_tree_attention_paged. */
+enum { MD_OUT_F32 = 0, MD_OUT_BF16 = 1 };
+
+MD_API md_status md_attention_paged_workspace(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t dh,
+                                              int32_t page_size, int32_t max_pages, size_t* bytes);
+
+/* md_tree_attention over a paged cache; a tree of one node is plain decoding.
+ *
+ *   out[b,t,h,:] = sum_j softmax_j( scale * q[b,t,h,:] . K[b,g,j,:] ) V[b,g,j,:]
+ *   over key slots j in [0, P_b) and P_b + a for every ancestor a of t
+ *   (t included), with P_b = prefix_len[b] and KV head g = h / (Hq / Hkv).
+ *
+ * q       [B, T, Hq, dh] bf16 (rotated, as md_qk_rope_append writes it).
+ * k_pages, v_pages [pool_pages, Hkv, page_size, dh] bf16; block_table
+ *         [B, max_pages]; slots [P_b, P_b + T) hold the tree's own K/V.
+ * prefix_len [B] int32; P_b + T > max_pages * page_size, or P_b < -1, sets
+ *         MD_DEV_BAD_PREFIX and writes zeros for that request. A bad page is
+ *         read as zeros.
+ * scale   softmax scale; 0 means 1/sqrt(dh).
+ * out     [B, T, Hq, dh] fp32 (MD_OUT_F32; weights kept to about 16 bits, as in
+ *         md_tree_attention) or bf16 (MD_OUT_BF16; weights rounded to bf16).
+ * q, k_pages, v_pages and out 16-byte aligned. The workspace is
+ * md_attention_paged_workspace()'s, 256-byte aligned, with any contents.
+ * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_WORKSPACE, MD_ERR_CUDA. */
+MD_API md_status md_tree_attention_paged(const md_bf16* q, const md_bf16* k_pages, const md_bf16* v_pages,
+                                         int32_t pool_pages, int32_t page_size, const int32_t* block_table,
+                                         int32_t max_pages, const int32_t* prefix_len, const md_tree* tree, int32_t B,
+                                         int32_t Hq, int32_t Hkv, int32_t dh, float scale, void* out,
+                                         int32_t out_type, void* ws, size_t ws_bytes, void* stream);
+
+/* Norms, rotation and cache write of new tokens: a step's tree or a prompt.
+ *
+ *   y          = x * rsqrt(mean_i(x_i^2) + eps) * w      (x itself without w)
+ *   (y_i, y_j) = (y_i cos a - y_j sin a, y_j cos a + y_i sin a),
+ *                a = pos[b,t] * inv_freq[f],
+ *                pairs (i, j) = (f, f + rot/2), or (2f, 2f + 1) if interleaved,
+ *                f in [0, rot/2); elements from rot on are not turned
+ *   q_out[b,t,h,:]                           <- y of q[b,t,h,:] with q_norm
+ *   K slot prefix_len[b] + t of request b    <- y of k[b,t,:,:] with k_norm
+ *   V slot prefix_len[b] + t of request b    <- v[b,t,:,:]
+ *
+ * in fp32 with one rounding to bf16 (the angle's turns in fp64), for
+ * t < n_new[b] (every t < T if n_new is NULL); other rows are left alone.
+ *
+ * q [B, T, Hq, dh], k, v [B, T, Hkv, dh] bf16, any views whose last dimension
+ *         is contiguous: `strides` is host [9], the element strides of request,
+ *         token and head of q, k and v in that order, multiples of 8.
+ * pos     [B, T] int32 position ids (md_tree_build's).
+ * inv_freq [rot/2] fp32; rot % 16 == 0, 16 <= rot <= dh.
+ * q_norm, k_norm [dh] bf16, each may be NULL. eps >= 0.
+ * q_out   [B, T, Hq, dh] bf16, dense; may be q itself where q is dense.
+ * A token whose slot does not fit its row of the table (or P_b < -1) sets
+ * MD_DEV_BAD_PREFIX; its K/V, or that of a bad page, is not written, its
+ * queries are. Pointers 16-byte aligned.
+ * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_CUDA. */
+MD_API md_status md_qk_rope_append(const md_bf16* q, const md_bf16* k, const md_bf16* v, const int64_t* strides,
+                                   const int32_t* pos, const float* inv_freq, int32_t rot, int32_t interleaved,
+                                   const md_bf16* q_norm, const md_bf16* k_norm, float eps, md_bf16* q_out,
+                                   md_bf16* k_pages, md_bf16* v_pages, int32_t pool_pages, int32_t page_size,
+                                   const int32_t* block_table, int32_t max_pages, const int32_t* prefix_len,
+                                   const int32_t* n_new, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t dh,
+                                   void* stream);
+
+/* md_tree_commit over a paged cache, for all layers of the model in one call.
+ *
+ * k_pages, v_pages [layers, pool_pages, Hkv, page_size, dh] bf16, updated in
+ * place; the other arguments and results are md_tree_commit's. An idle slot
+ * gives -1, -1, -1. A bad length, path or prefix (MD_DEV_BAD_PATH), or a bad
+ * page under a row that moves (MD_DEV_BAD_PAGE), leaves that request's cache
+ * unchanged (new_prefix_len = P, next_head_row = -1).
+ * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED (dh not 64/128), MD_ERR_CUDA. */
+MD_API md_status md_tree_commit_paged(md_bf16* k_pages, md_bf16* v_pages, int32_t layers, int32_t pool_pages,
+                                      int32_t page_size, const int32_t* block_table, int32_t max_pages, int32_t Hkv,
+                                      int32_t dh, const md_tree* tree, int32_t B, const int32_t* prefix_len,
+                                      const int32_t* accept_len, const int32_t* path, int32_t K,
+                                      const int32_t* bonus, int32_t* new_prefix_len, int32_t* next_root,
+                                      int32_t* next_head_row, void* stream);
+
+/* Gives every request the pages for length[b] + extra slots, in place: rows
+ * that hold more give their last pages back (entries become -1), then the
+ * lowest free pages go to the rows that need more, in row order.
+ *
+ *   wanted[b] = 0 if length[b] < 0, else ceil((length[b] + extra) / page_size)
+ *
+ * block_table [B, max_pages], n_pages [B] (pages a row holds), refcount
+ * [pool_pages] (rows that hold a page; 0 = free) int32; 16-byte aligned
+ * refcount. extra >= 0. A row is served if its need and those of the rows
+ * before it fit the free pages; the others keep what they hold and
+ * MD_DEV_NO_PAGES is set. A row whose wanted pages exceed max_pages
+ * (MD_DEV_BAD_PREFIX) or whose n_pages is not in [0, max_pages]
+ * (MD_DEV_BAD_PAGE) is left alone. length = -1 frees a row. B <= 16384.
+ * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_CUDA. */
+MD_API md_status md_pages_resize(int32_t* block_table, int32_t* n_pages, int32_t* refcount, const int32_t* length,
+                                 int32_t B, int32_t max_pages, int32_t pool_pages, int32_t page_size, int32_t extra,
+                                 void* stream);
+
+/* Workspace bytes md_pages_fork needs for n forks. */
+MD_API md_status md_pages_fork_workspace(int32_t B, int32_t n, size_t* bytes);
+
+/* Continues sequences twice: row dst[i] becomes a copy of row src[i].
+ * dst's former pages are given back first; src's full pages are then shared
+ * (their count grows), and the page that length[src] ends inside is copied, its
+ * used slots of every layer, to a new one (the lowest free pages, in list
+ * order), so that each sequence writes pages of its own from there on.
+ *
+ * src, dst [n] int32 rows, n <= 1024; src[i] = -1 is an unused entry. A row
+ * outside [0, B), a dst that is also a src or an earlier dst of the call sets
+ * MD_DEV_BAD_ROW and its fork is left out. One src may have several dst.
+ * length [B] int32: length[dst] = length[src] (updated in place; a negative
+ * length empties dst). length[src] > n_pages[src] * page_size
+ * (MD_DEV_BAD_PREFIX) or an impossible n_pages (MD_DEV_BAD_PAGE) leaves the fork
+ * out. Without a free page (MD_DEV_NO_PAGES) dst ends empty, length -1.
+ * k_pages, v_pages [layers, pool_pages, Hkv, page_size, dh] bf16; the table
+ * arrays as in md_pages_resize. Workspace 256-byte aligned, any contents.
+ * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_WORKSPACE, MD_ERR_CUDA. */
+MD_API md_status md_pages_fork(md_bf16* k_pages, md_bf16* v_pages, int32_t layers, int32_t pool_pages, int32_t Hkv,
+                               int32_t page_size, int32_t dh, int32_t* block_table, int32_t* n_pages,
+                               int32_t* refcount, int32_t* length, int32_t B, int32_t max_pages, const int32_t* src,
+                               const int32_t* dst, int32_t n, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Status.                                                                   */

@@ -19,6 +19,8 @@ LIB_PATH = os.path.join(HERE, "libmedusa.so")
 MD_ACCEPT_GREEDY = 0
 MD_ACCEPT_TYPICAL = 1
 DEV_BAD_PREFIX, DEV_BAD_ROW, DEV_BAD_TOKEN, DEV_TIMEOUT, DEV_BAD_PATH = 1, 2, 4, 8, 16
+DEV_BAD_PAGE, DEV_NO_PAGES = 32, 64
+MD_OUT_F32, MD_OUT_BF16 = 0, 1
 
 _lib = None
 _P = ctypes.c_void_p
@@ -46,6 +48,14 @@ _SIGNATURES = {
     "md_tree_accept_sampled": [_P, _I, _P, _P, _I, _I, _F, _P, _P, _P, _P, _P, _SZ, _P],
     "md_tree_accept_rejection": [_P, _I, _P, _P, _I, _I, _F, _P, _I, _I, _P, _F, _P, _P, _P, _P, _P, _P],
     "md_tree_commit": [_P, _P, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P],
+    "md_attention_paged_workspace": [_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)],
+    "md_tree_attention_paged": [_P, _P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I, _F, _P, _I, _P, _SZ, _P],
+    "md_qk_rope_append": [_P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _F, _P, _P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _I,
+                          _I, _I, _P],
+    "md_tree_commit_paged": [_P, _P, _I, _I, _I, _P, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P],
+    "md_pages_resize": [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P],
+    "md_pages_fork_workspace": [_I, _I, ctypes.POINTER(_SZ)],
+    "md_pages_fork": [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _P, _I, _P, _SZ, _P],
     "md_get_device_status": [_P, ctypes.POINTER(_I), _I],
     "md_set_wait_limit": [ctypes.c_uint64],
     "md_stream_read": [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p],
@@ -392,6 +402,188 @@ def tree_commit(k_cache, v_cache, tree: Tree, prefix_len, accept_len, path, bonu
         _ptr(new_prefix_len, torch.int32, "new_prefix_len"), _ptr(next_root, torch.int32, "next_root"),
         _ptr(next_head_row, torch.int32, "next_head_row"), _stream(stream))
     _check(rc, "md_tree_commit")
+
+
+# ---------------------------------------------------------------------------
+# The step over a paged KV cache.
+# ---------------------------------------------------------------------------
+
+class _on_device:
+    """Makes the device of a call's tensors current while it launches: checks
+    that all of them (None aside) live on one, and picks that device's current
+    stream unless the caller gave one."""
+
+    def __init__(self, what, stream, **tensors):
+        devs = {name: t.device for name, t in tensors.items() if isinstance(t, torch.Tensor)}
+        first = next(iter(devs.values()))
+        for name, d in devs.items():
+            if d != first:
+                raise ValueError(f"{what}: {name} is on {d}, expected {first}")
+        self.device, self.stream = first, stream
+
+    def __enter__(self):
+        self.guard = torch.cuda.device(self.device)
+        self.guard.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream if self.stream is None else _stream(self.stream)
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def _pools(what, k_pages, v_pages, layered):
+    """(layers, pool_pages, Hkv, page_size, dh) of a pair of pools."""
+    dims = (4, 5) if layered else (4,)
+    if k_pages.dim() not in dims:
+        raise ValueError(f"{what}: k_pages has {k_pages.dim()} dims, expected "
+                         + ("[pages, Hkv, page_size, dh] or [layers, pages, Hkv, page_size, dh]" if layered
+                            else "[pages, Hkv, page_size, dh]"))
+    _same(what, v_pages=(tuple(v_pages.shape), tuple(k_pages.shape)))
+    shape = tuple(k_pages.shape)
+    return shape if len(shape) == 5 else (1,) + shape
+
+
+def attention_paged_workspace_bytes(B, T, Hq, Hkv, dh, page_size, max_pages) -> int:
+    n = _SZ()
+    _check(lib().md_attention_paged_workspace(B, T, Hq, Hkv, dh, page_size, max_pages, ctypes.byref(n)),
+           "md_attention_paged_workspace")
+    return n.value
+
+
+def tree_attention_paged(q, k_pages, v_pages, block_table, prefix_len, tree: Tree, out, ws, scale=0.0, stream=None):
+    """md_tree_attention_paged: q [B,T,Hq,dh], pools [pages,Hkv,page_size,dh] bf16, block_table
+    [B,max_pages] int32 -> out [B,T,Hq,dh], fp32 or bf16 (by its dtype). prefix_len -1: an idle slot."""
+    B, T, Hq, dh = q.shape
+    _, pages, Hkv, page, dhk = _pools("tree_attention_paged", k_pages, v_pages, layered=False)
+    _same("tree_attention_paged", T=(T, tree.T), k_pages_dh=(dhk, dh), block_table_rows=(block_table.shape[0], B),
+          prefix_len=(tuple(prefix_len.shape), (B,)), out=(tuple(out.shape), (B, T, Hq, dh)))
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"out: expected torch.float32 or torch.bfloat16, got {out.dtype}")
+    args = (_ptr(q, torch.bfloat16, "q", 4), _ptr(k_pages, torch.bfloat16, "k_pages", 4),
+            _ptr(v_pages, torch.bfloat16, "v_pages", 4), pages, page, _ptr(block_table, torch.int32, "block_table", 2),
+            block_table.shape[1], _ptr(prefix_len, torch.int32, "prefix_len"), tree.handle, B, Hq, Hkv, dh, float(scale),
+            _ptr(out, out.dtype, "out", 4), MD_OUT_BF16 if out.dtype == torch.bfloat16 else MD_OUT_F32,
+            _ptr(ws, torch.uint8, "ws"), ws.numel())
+    with _on_device("tree_attention_paged", stream, q=q, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
+                    prefix_len=prefix_len, out=out, ws=ws) as st:
+        rc = lib().md_tree_attention_paged(*args, st)
+    _check(rc, "md_tree_attention_paged")
+
+
+def _head_rows(t, name, B, T, H, dh):
+    """Pointer and element strides (request, token, head) of a [B,T,H,dh] view
+    whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    _same("qk_rope_append", **{name: (tuple(t.shape), (B, T, H, dh))})
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # a dimension of size 1 is never stepped over: its stride may be anything
+    strides = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
+    if any(s % 8 for s in strides) or t.data_ptr() % 16:
+        raise ValueError(f"{name}: rows must start on 16-byte boundaries")
+    return t.data_ptr(), strides
+
+
+def qk_rope_append(q, k, v, pos, inv_freq, q_out, k_pages, v_pages, block_table, prefix_len, q_norm=None, k_norm=None,
+                   eps=1e-6, interleaved=False, n_new=None, stream=None):
+    """md_qk_rope_append: per-head norms (q_norm, k_norm [dh] bf16, optional) and rotation by
+    pos [B,T] * inv_freq [rot/2] of q [B,T,Hq,dh] into q_out (dense) and of k [B,T,Hkv,dh] into
+    slots prefix_len[b] + t of the pools, v beside it. q, k, v: bf16 views (of one fused
+    projection, say). n_new [B]: tokens of each request (the rest of T is padding)."""
+    B, T, Hq, dh = q.shape
+    Hkv = k.shape[2]
+    _, pages, hk, page, dhk = _pools("qk_rope_append", k_pages, v_pages, layered=False)
+    _same("qk_rope_append", k_pages=((hk, dhk), (Hkv, dh)), pos=(tuple(pos.shape), (B, T)),
+          q_out=(tuple(q_out.shape), (B, T, Hq, dh)), block_table_rows=(block_table.shape[0], B),
+          prefix_len=(tuple(prefix_len.shape), (B,)))
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None:
+            _same("qk_rope_append", **{name: (tuple(w.shape), (dh,))})
+    if n_new is not None:
+        _same("qk_rope_append", n_new=(tuple(n_new.shape), (B,)))
+    qp, qs = _head_rows(q, "q", B, T, Hq, dh)
+    kp, ks = _head_rows(k, "k", B, T, Hkv, dh)
+    vp, vs = _head_rows(v, "v", B, T, Hkv, dh)
+    strides = (ctypes.c_int64 * 9)(*qs, *ks, *vs)
+    args = (qp, kp, vp, strides, _ptr(pos, torch.int32, "pos"), _ptr(inv_freq, torch.float32, "inv_freq", 1),
+            2 * inv_freq.shape[0], int(bool(interleaved)), _ptr(q_norm, torch.bfloat16, "q_norm"),
+            _ptr(k_norm, torch.bfloat16, "k_norm"), float(eps), _ptr(q_out, torch.bfloat16, "q_out"),
+            _ptr(k_pages, torch.bfloat16, "k_pages"), _ptr(v_pages, torch.bfloat16, "v_pages"), pages, page,
+            _ptr(block_table, torch.int32, "block_table", 2), block_table.shape[1],
+            _ptr(prefix_len, torch.int32, "prefix_len"), _ptr(n_new, torch.int32, "n_new"), B, T, Hq, Hkv, dh)
+    with _on_device("qk_rope_append", stream, q=q, k=k, v=v, pos=pos, inv_freq=inv_freq, q_out=q_out, k_pages=k_pages,
+                    v_pages=v_pages, block_table=block_table, prefix_len=prefix_len, q_norm=q_norm, k_norm=k_norm,
+                    n_new=n_new) as st:
+        rc = lib().md_qk_rope_append(*args, st)
+    _check(rc, "md_qk_rope_append")
+
+
+def tree_commit_paged(k_pages, v_pages, block_table, tree: Tree, prefix_len, accept_len, path, bonus, new_prefix_len,
+                      next_root, next_head_row, stream=None):
+    """md_tree_commit_paged: tree_commit over pools [pages,Hkv,page_size,dh], or
+    [layers,pages,Hkv,page_size,dh] for every layer at once (in place)."""
+    B = block_table.shape[0]
+    layers, pages, Hkv, page, dh = _pools("tree_commit_paged", k_pages, v_pages, layered=True)
+    K = path.shape[1] - 1
+    _same("tree_commit_paged", path_rows=(path.shape[0], B), prefix_len=(tuple(prefix_len.shape), (B,)),
+          accept_len=(tuple(accept_len.shape), (B,)), bonus=(tuple(bonus.shape), (B,)),
+          new_prefix_len=(tuple(new_prefix_len.shape), (B,)), next_root=(tuple(next_root.shape), (B,)),
+          next_head_row=(tuple(next_head_row.shape), (B,)))
+    args = (_ptr(k_pages, torch.bfloat16, "k_pages"), _ptr(v_pages, torch.bfloat16, "v_pages"), layers, pages, page,
+            _ptr(block_table, torch.int32, "block_table", 2), block_table.shape[1], Hkv, dh, tree.handle, B,
+            _ptr(prefix_len, torch.int32, "prefix_len"), _ptr(accept_len, torch.int32, "accept_len"),
+            _ptr(path, torch.int32, "path", 2), K, _ptr(bonus, torch.int32, "bonus"),
+            _ptr(new_prefix_len, torch.int32, "new_prefix_len"), _ptr(next_root, torch.int32, "next_root"),
+            _ptr(next_head_row, torch.int32, "next_head_row"))
+    with _on_device("tree_commit_paged", stream, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
+                    prefix_len=prefix_len, accept_len=accept_len, path=path, bonus=bonus, new_prefix_len=new_prefix_len,
+                    next_root=next_root, next_head_row=next_head_row) as st:
+        rc = lib().md_tree_commit_paged(*args, st)
+    _check(rc, "md_tree_commit_paged")
+
+
+def pages_resize(block_table, n_pages, refcount, length, page_size, extra=0, stream=None):
+    """md_pages_resize: rows of block_table [B,max_pages] grow (lowest free pages of refcount
+    [pages] in row order) or shrink to ceil((length + extra) / page_size) pages, in place.
+    length [B]; -1 frees the row."""
+    B, width = block_table.shape
+    _same("pages_resize", n_pages=(tuple(n_pages.shape), (B,)), length=(tuple(length.shape), (B,)))
+    args = (_ptr(block_table, torch.int32, "block_table", 2), _ptr(n_pages, torch.int32, "n_pages"),
+            _ptr(refcount, torch.int32, "refcount", 1), _ptr(length, torch.int32, "length"), B, width, refcount.shape[0],
+            int(page_size), int(extra))
+    with _on_device("pages_resize", stream, block_table=block_table, n_pages=n_pages, refcount=refcount,
+                    length=length) as st:
+        rc = lib().md_pages_resize(*args, st)
+    _check(rc, "md_pages_resize")
+
+
+def pages_fork_workspace_bytes(B, n) -> int:
+    size = _SZ()
+    _check(lib().md_pages_fork_workspace(B, n, ctypes.byref(size)), "md_pages_fork_workspace")
+    return size.value
+
+
+def pages_fork(k_pages, v_pages, block_table, n_pages, refcount, src, dst, length, ws, stream=None):
+    """md_pages_fork: row dst[i] of the table becomes a copy of row src[i]: full pages shared, the
+    last, partly filled one copied in every layer of the pools ([pages,Hkv,page_size,dh] or
+    [layers,...]). length [B] is updated; src[i] = -1 is an unused entry."""
+    B, width = block_table.shape
+    layers, pages, Hkv, page, dh = _pools("pages_fork", k_pages, v_pages, layered=True)
+    _same("pages_fork", n_pages=(tuple(n_pages.shape), (B,)), length=(tuple(length.shape), (B,)),
+          refcount=(tuple(refcount.shape), (pages,)), dst=(tuple(dst.shape), (src.shape[0],)))
+    args = (_ptr(k_pages, torch.bfloat16, "k_pages"), _ptr(v_pages, torch.bfloat16, "v_pages"), layers, pages, Hkv, page,
+            dh, _ptr(block_table, torch.int32, "block_table", 2), _ptr(n_pages, torch.int32, "n_pages"),
+            _ptr(refcount, torch.int32, "refcount", 1), _ptr(length, torch.int32, "length"), B, width,
+            _ptr(src, torch.int32, "src", 1), _ptr(dst, torch.int32, "dst", 1), src.shape[0],
+            _ptr(ws, torch.uint8, "ws"), ws.numel())
+    with _on_device("pages_fork", stream, k_pages=k_pages, v_pages=v_pages, block_table=block_table, n_pages=n_pages,
+                    refcount=refcount, src=src, dst=dst, length=length, ws=ws) as st:
+        rc = lib().md_pages_fork(*args, st)
+    _check(rc, "md_pages_fork")
 
 
 def device_status(clear: bool = True, stream=None) -> int:

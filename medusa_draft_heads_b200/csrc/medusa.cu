@@ -19,6 +19,10 @@
 #include "attention_tc.cuh"
 #include "accept.cuh"
 #include "commit.cuh"
+#include "append.cuh"
+#include "attention_paged.cuh"
+#include "commit_paged.cuh"
+#include "pages.cuh"
 #include "hydra.cuh"
 #include "reject.cuh"
 
@@ -1439,6 +1443,162 @@ md_status md_tree_commit(md_bf16* k_cache, md_bf16* v_cache, int32_t S_max, int3
   const int smem = 2 * (MD_MAX_K + 1) * dh * 2;
   return launch_pdl(md::commit::tree_commit_kernel, dim3(Hkv, B), dim3(md::commit::kThreads), smem,
                     static_cast<cudaStream_t>(stream), tree->tp, a);
+}
+
+// ------------------------------- paged cache -------------------------------
+
+namespace {
+
+// Sizes every paged call checks: a pool whose page rows a 32-bit TMA coordinate reaches.
+md_status paged_check(int32_t B, int32_t pool_pages, int32_t page_size, int32_t max_pages, int32_t Hkv, int32_t dh) {
+  if (B < 1 || pool_pages < 1 || page_size < 1 || max_pages < 1 || Hkv < 1) return MD_ERR_INVALID_ARG;
+  if (dh != 64 && dh != 128) return MD_ERR_UNSUPPORTED;
+  if (B > 65535 || int64_t(pool_pages) * Hkv > INT32_MAX || int64_t(max_pages) * page_size > INT32_MAX)
+    return MD_ERR_UNSUPPORTED;
+  return MD_OK;
+}
+
+}  // namespace
+
+md_status md_attention_paged_workspace(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t dh, int32_t page_size,
+                                       int32_t max_pages, size_t* bytes) {
+  if (!bytes || T < 1 || Hq < 1) return MD_ERR_INVALID_ARG;
+  md_status s = paged_check(B, 1, page_size, max_pages, Hkv, dh);
+  if (s != MD_OK) return s;
+  if (T > MD_MAX_T || Hq % Hkv != 0 || Hq / Hkv > 16 || page_size % 16 != 0) return MD_ERR_UNSUPPORTED;
+  *bytes = 256;
+  return MD_OK;
+}
+
+md_status md_tree_attention_paged(const md_bf16* q, const md_bf16* k_pages, const md_bf16* v_pages, int32_t pool_pages,
+                                  int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                                  const int32_t* prefix_len, const md_tree* tree, int32_t B, int32_t Hq, int32_t Hkv,
+                                  int32_t dh, float scale, void* out, int32_t out_type, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  if (!q || !k_pages || !v_pages || !block_table || !prefix_len || !tree || !out) return MD_ERR_INVALID_ARG;
+  size_t need = 0;
+  md_status s = md_attention_paged_workspace(B, tree->tp.T, Hq, Hkv, dh, page_size, max_pages, &need);
+  if (s != MD_OK) return s;
+  if ((s = paged_check(B, pool_pages, page_size, max_pages, Hkv, dh)) != MD_OK) return s;
+  if (!(scale >= 0.f) || !std::isfinite(scale) || (out_type != MD_OUT_F32 && out_type != MD_OUT_BF16))
+    return MD_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16)) return MD_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < need || !aligned(ws, 256)) return MD_ERR_WORKSPACE;
+  md::attn_paged::Args a;
+  a.q = q; a.kp = k_pages; a.vp = v_pages; a.table = block_table; a.prefix_len = prefix_len; a.out = out;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.pool = pool_pages; a.page = page_size; a.max_pages = max_pages;
+  a.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(float(dh))) * 1.4426950408889634f;
+  a.out_bf16 = out_type == MD_OUT_BF16;
+  const dim3 grid((tree->tp.T * Hq + 3) / 4, B);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return dh == 128 ? launch_pdl(md::attn_paged::attn_paged_rows_kernel<128>, grid, dim3(md::attn_paged::kThreads), 0, st,
+                                tree->tp, a)
+                   : launch_pdl(md::attn_paged::attn_paged_rows_kernel<64>, grid, dim3(md::attn_paged::kThreads), 0, st,
+                                tree->tp, a);
+}
+
+md_status md_qk_rope_append(const md_bf16* q, const md_bf16* k, const md_bf16* v, const int64_t* strides,
+                            const int32_t* pos, const float* inv_freq, int32_t rot, int32_t interleaved,
+                            const md_bf16* q_norm, const md_bf16* k_norm, float eps, md_bf16* q_out, md_bf16* k_pages,
+                            md_bf16* v_pages, int32_t pool_pages, int32_t page_size, const int32_t* block_table,
+                            int32_t max_pages, const int32_t* prefix_len, const int32_t* n_new, int32_t B, int32_t T,
+                            int32_t Hq, int32_t Hkv, int32_t dh, void* stream) {
+  if (!q || !k || !v || !strides || !pos || !inv_freq || !q_out || !k_pages || !v_pages || !block_table || !prefix_len)
+    return MD_ERR_INVALID_ARG;
+  if (T < 1 || Hq < 1 || !(eps >= 0.f) || !std::isfinite(eps)) return MD_ERR_INVALID_ARG;
+  md_status s = paged_check(B, pool_pages, page_size, max_pages, Hkv, dh);
+  if (s != MD_OK) return s;
+  if (rot < 16 || rot > dh || rot % 16 != 0 || int64_t(B) * T > INT32_MAX || int64_t(Hq) + 2 * int64_t(Hkv) > 65535)
+    return MD_ERR_UNSUPPORTED;
+  const void* ptrs[] = {q, k, v, q_out, k_pages, v_pages, q_norm, k_norm};
+  for (const void* p : ptrs)
+    if (!aligned(p, 16)) return MD_ERR_INVALID_ARG;
+  for (int i = 0; i < 9; ++i)
+    if (strides[i] % 8 != 0) return MD_ERR_INVALID_ARG;
+  md::append::Args a;
+  a.q = q; a.k = k; a.v = v;
+  a.qb = strides[0]; a.qt = strides[1]; a.qh = strides[2];
+  a.kb = strides[3]; a.kt = strides[4]; a.kh = strides[5];
+  a.vb = strides[6]; a.vt = strides[7]; a.vh = strides[8];
+  a.pos = pos; a.inv_freq = inv_freq; a.q_norm = q_norm; a.k_norm = k_norm; a.q_out = q_out;
+  a.k_pages = k_pages; a.v_pages = v_pages; a.table = block_table; a.prefix_len = prefix_len; a.n_new = n_new;
+  a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.rot = rot; a.interleaved = interleaved != 0;
+  a.max_pages = max_pages; a.pool = pool_pages; a.page = page_size; a.eps = eps;
+  const dim3 grid(B * T, 1);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return dh == 128 ? launch_pdl(md::append::qk_rope_append_kernel<128>, grid, dim3(md::append::kThreads), 0, st, a)
+                   : launch_pdl(md::append::qk_rope_append_kernel<64>, grid, dim3(md::append::kThreads), 0, st, a);
+}
+
+md_status md_tree_commit_paged(md_bf16* k_pages, md_bf16* v_pages, int32_t layers, int32_t pool_pages,
+                               int32_t page_size, const int32_t* block_table, int32_t max_pages, int32_t Hkv,
+                               int32_t dh, const md_tree* tree, int32_t B, const int32_t* prefix_len,
+                               const int32_t* accept_len, const int32_t* path, int32_t K, const int32_t* bonus,
+                               int32_t* new_prefix_len, int32_t* next_root, int32_t* next_head_row, void* stream) {
+  if (!k_pages || !v_pages || !block_table || !tree || !prefix_len || !accept_len || !path || !bonus ||
+      !new_prefix_len || !next_root || !next_head_row)
+    return MD_ERR_INVALID_ARG;
+  if (layers < 1 || K < tree->tp.max_depth || K > MD_MAX_K) return MD_ERR_INVALID_ARG;
+  md_status s = paged_check(B, pool_pages, page_size, max_pages, Hkv, dh);
+  if (s != MD_OK) return s;
+  if (new_prefix_len == prefix_len || !aligned(k_pages, 16) || !aligned(v_pages, 16)) return MD_ERR_INVALID_ARG;
+  md::commit_paged::Args a;
+  a.kp = reinterpret_cast<uint4*>(k_pages); a.vp = reinterpret_cast<uint4*>(v_pages);
+  a.table = block_table; a.prefix_len = prefix_len; a.accept_len = accept_len; a.path = path; a.bonus = bonus;
+  a.new_prefix_len = new_prefix_len; a.next_root = next_root; a.next_head_row = next_head_row;
+  a.layers = layers; a.pool = pool_pages; a.page = page_size; a.max_pages = max_pages; a.Hkv = Hkv; a.row16 = dh / 8;
+  a.K = K;
+  const int64_t cols = int64_t(2) * layers * Hkv * a.row16;
+  const int64_t blocks = (cols + md::commit_paged::kThreads - 1) / md::commit_paged::kThreads;
+  return launch_pdl(md::commit_paged::tree_commit_paged_kernel, dim3(unsigned(std::min<int64_t>(blocks, 1 << 20)), B),
+                    dim3(md::commit_paged::kThreads), 0, static_cast<cudaStream_t>(stream), tree->tp, a);
+}
+
+md_status md_pages_resize(int32_t* block_table, int32_t* n_pages, int32_t* refcount, const int32_t* length, int32_t B,
+                          int32_t max_pages, int32_t pool_pages, int32_t page_size, int32_t extra, void* stream) {
+  if (!block_table || !n_pages || !refcount || !length || extra < 0) return MD_ERR_INVALID_ARG;
+  md_status s = paged_check(B, pool_pages, page_size, max_pages, 1, 64);
+  if (s != MD_OK) return s;
+  if (B > md::pages::kMaxRows) return MD_ERR_UNSUPPORTED;
+  if (!aligned(refcount, 16)) return MD_ERR_INVALID_ARG;
+  md::pages::ResizeArgs a;
+  a.table = block_table; a.n_pages = n_pages; a.refcount = refcount; a.length = length;
+  a.B = B; a.max_pages = max_pages; a.pool = pool_pages; a.page = page_size; a.extra = extra;
+  const int smem = B * 4;
+  if (smem > 32768 && (s = set_smem(md::pages::pages_resize_kernel, md::pages::kMaxRows * 4)) != MD_OK) return s;
+  return launch_pdl(md::pages::pages_resize_kernel, dim3(1), dim3(md::pages::kThreads), smem,
+                    static_cast<cudaStream_t>(stream), a);
+}
+
+md_status md_pages_fork_workspace(int32_t B, int32_t n, size_t* bytes) {
+  if (!bytes || B < 1 || n < 1) return MD_ERR_INVALID_ARG;
+  if (n > md::pages::kMaxForks) return MD_ERR_UNSUPPORTED;
+  *bytes = md::heads::align256(size_t(n) * sizeof(md::pages::ForkJob));
+  return MD_OK;
+}
+
+md_status md_pages_fork(md_bf16* k_pages, md_bf16* v_pages, int32_t layers, int32_t pool_pages, int32_t Hkv,
+                        int32_t page_size, int32_t dh, int32_t* block_table, int32_t* n_pages, int32_t* refcount,
+                        int32_t* length, int32_t B, int32_t max_pages, const int32_t* src, const int32_t* dst,
+                        int32_t n, void* ws, size_t ws_bytes, void* stream) {
+  if (!k_pages || !v_pages || !block_table || !n_pages || !refcount || !length || !src || !dst) return MD_ERR_INVALID_ARG;
+  size_t need = 0;
+  md_status s = md_pages_fork_workspace(B, n, &need);
+  if (s != MD_OK) return s;
+  if (layers < 1) return MD_ERR_INVALID_ARG;
+  if ((s = paged_check(B, pool_pages, page_size, max_pages, Hkv, dh)) != MD_OK) return s;
+  if (int64_t(layers) * Hkv > INT32_MAX) return MD_ERR_UNSUPPORTED;
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(refcount, 16)) return MD_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < need || !aligned(ws, 256)) return MD_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  md::pages::ForkArgs a;
+  a.table = block_table; a.n_pages = n_pages; a.refcount = refcount; a.length = length; a.src = src; a.dst = dst;
+  a.jobs = static_cast<md::pages::ForkJob*>(ws);
+  a.B = B; a.n = n; a.max_pages = max_pages; a.pool = pool_pages; a.page = page_size;
+  if ((s = launch_pdl(md::pages::pages_fork_kernel, dim3(1), dim3(md::pages::kThreads), 0, st, a)) != MD_OK) return s;
+  return launch_pdl(md::pages::pages_fork_copy_kernel, dim3(layers * Hkv, 2, n), dim3(256), 0, st,
+                    reinterpret_cast<uint4*>(k_pages), reinterpret_cast<uint4*>(v_pages),
+                    static_cast<const md::pages::ForkJob*>(a.jobs), pool_pages, Hkv, page_size, dh / 8);
 }
 
 md_status md_get_device_status(void* stream, int32_t* out, int32_t clear) {

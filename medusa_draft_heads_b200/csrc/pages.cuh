@@ -1,0 +1,338 @@
+// The pages of a paged KV cache: which request holds which page, and the
+// copying of a page when a sequence forks.
+//
+// Book-keeping lives on the device, in three int32 arrays that a step's calls
+// read and write in stream order, so a decode loop never waits for the host:
+// block_table [B, max_pages] (page ids, -1 past a row's pages), n_pages [B] and
+// refcount [pool]. A page is free iff its count is 0, and requests get the
+// lowest free ids in row order: every result follows from the arrays alone,
+// whatever order the atomics ran in (they only add and subtract integers).
+#pragma once
+
+#include "common.cuh"
+
+namespace md {
+namespace pages {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kPerThread = 4;                    // counts per thread and scan tile
+constexpr int kTile = kThreads * kPerThread;
+constexpr int kMaxRows = 16384;                  // rows of a resize: their running needs sit in shared memory
+constexpr int kMaxForks = kThreads;              // forks of a call: one thread each
+
+__device__ __forceinline__ int warp_incl_scan(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+// Inclusive sum over the block's threads; `total` receives the block's sum.
+// `part` is kWarps ints of shared memory; all threads call it.
+__device__ __forceinline__ int block_incl_scan(int v, int* part, int& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  v = warp_incl_scan(v);
+  __syncthreads();                               // the previous scan's sums have been read
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  if (warp == 0) part[lane] = warp_incl_scan(part[lane]);
+  __syncthreads();
+  total = part[kWarps - 1];
+  return v + (warp > 0 ? part[warp - 1] : 0);
+}
+
+// Drops one reference to a page. A page that is not in the pool, or that
+// nobody holds, is flagged and its count stays.
+__device__ __forceinline__ void drop_page(int32_t* refcount, int pool, int page) {
+  if (page < 0 || page >= pool) {
+    set_status(MD_DEV_BAD_PAGE);
+    return;
+  }
+  if (atomicSub(&refcount[page], 1) <= 0) {
+    atomicAdd(&refcount[page], 1);
+    set_status(MD_DEV_BAD_PAGE);
+  }
+}
+
+// Bit i of the result: page (tile base + kPerThread * threadIdx.x + i) is free.
+// Counts are read past L1: the block's own atomics may just have changed them.
+__device__ __forceinline__ uint32_t free_bits(const int32_t* refcount, int pool, int base) {
+  const int p0 = base + int(threadIdx.x) * kPerThread;
+  uint32_t m = 0;
+  if (p0 + kPerThread <= pool) {
+    const int4 c = __ldcg(reinterpret_cast<const int4*>(refcount + p0));
+    m = (c.x == 0 ? 1u : 0u) | (c.y == 0 ? 2u : 0u) | (c.z == 0 ? 4u : 0u) | (c.w == 0 ? 8u : 0u);
+  } else {
+    for (int i = 0; i < kPerThread; ++i)
+      if (p0 + i < pool && __ldcg(refcount + p0 + i) == 0) m |= 1u << i;
+  }
+  return m;
+}
+
+// Free pages of the pool, counted by the whole block.
+__device__ __forceinline__ int count_free(const int32_t* refcount, int pool, int* part) {
+  int n = 0;
+  for (int base = 0; base < pool; base += kTile) n += __popc(free_bits(refcount, pool, base));
+  int total;
+  block_incl_scan(n, part, total);
+  return total;
+}
+
+// Calls take(rank, page) for the `want` lowest free pages (rank 0 .. want - 1).
+template <typename Take>
+__device__ __forceinline__ void take_lowest_free(const int32_t* refcount, int pool, int want, int* part, Take take) {
+  int seen = 0;
+  for (int base = 0; base < pool && seen < want; base += kTile) {   // uniform over the block
+    const uint32_t m = free_bits(refcount, pool, base);
+    const int n = __popc(m);
+    int total;
+    int rank = seen + block_incl_scan(n, part, total) - n;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      if ((m >> i) & 1u) {
+        if (rank < want) take(rank, base + int(threadIdx.x) * kPerThread + i);
+        ++rank;
+      }
+    }
+    seen += total;
+  }
+}
+
+// ------------------------------------------------------------------ resize
+
+struct ResizeArgs {
+  int32_t* table;           // [B, max_pages]
+  int32_t* n_pages;         // [B]
+  int32_t* refcount;        // [pool]
+  const int32_t* length;    // [B]
+  int B, max_pages, pool, page, extra;
+};
+
+// Pages row b should hold, or -1 if the row is to be left alone (its count or
+// its length cannot be right).
+__device__ __forceinline__ int wanted_pages(const ResizeArgs& a, int b, int held) {
+  if (held < 0 || held > a.max_pages) return -1;
+  const int len = a.length[b];
+  if (len < 0) return 0;
+  const long long want = ((long long)len + a.extra + a.page - 1) / a.page;
+  return want > a.max_pages ? -1 : int(want);
+}
+
+// One CTA. Rows that hold too much give their last pages back, then the lowest
+// free pages go to the rows that need more, in row order. A few KB of traffic
+// plus 4 B per page of the pool (read when some row needs a page): latency-bound.
+__global__ void __launch_bounds__(kThreads) pages_resize_kernel(ResizeArgs a) {
+  pdl_wait_primary();          // lengths come from the previous kernels
+  pdl_launch_dependents();
+  extern __shared__ int32_t upto[];              // [B]: pages needed by rows 0 .. b
+  __shared__ int part[kWarps];
+  __shared__ int served_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  for (int b = warp; b < a.B; b += kWarps) {     // a warp per row: give back
+    const int held = a.n_pages[b];
+    const int want = wanted_pages(a, b, held);
+    if (want < 0) {
+      if (lane == 0) set_status(held < 0 || held > a.max_pages ? MD_DEV_BAD_PAGE : MD_DEV_BAD_PREFIX);
+      continue;
+    }
+    int32_t* row = a.table + size_t(b) * a.max_pages;
+    for (int i = want + lane; i < held; i += 32) {
+      drop_page(a.refcount, a.pool, row[i]);
+      row[i] = -1;
+    }
+    __syncwarp();
+    if (lane == 0 && held > want) a.n_pages[b] = want;
+  }
+  __syncthreads();
+
+  int all = 0;                                   // running needs of the rows
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int need = 0;
+    if (b < a.B) {
+      const int held = a.n_pages[b];
+      need = max(0, wanted_pages(a, b, held) - held);
+    }
+    int total;
+    const int incl = block_incl_scan(need, part, total);
+    if (b < a.B) upto[b] = all + incl;
+    all += total;
+  }
+  if (all == 0) return;
+  const int free_pages = count_free(a.refcount, a.pool, part);
+  // rows are served as long as their needs and those of the rows before them fit
+  if (threadIdx.x == 0) served_s = all;
+  __syncthreads();
+  if (all > free_pages) {
+    if (threadIdx.x == 0) {
+      int lo = 0, hi = a.B;                      // rows [0, lo) fit
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (upto[mid] <= free_pages) lo = mid + 1; else hi = mid;
+      }
+      served_s = lo > 0 ? upto[lo - 1] : 0;
+      set_status(MD_DEV_NO_PAGES);
+    }
+    __syncthreads();
+  }
+  const int served = served_s;
+  take_lowest_free(a.refcount, a.pool, served, part, [&](int rank, int page) {
+    int lo = 0, hi = a.B - 1;                    // the first row whose running need exceeds the rank
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (upto[mid] > rank) hi = mid; else lo = mid + 1;
+    }
+    const int before = lo > 0 ? upto[lo - 1] : 0;
+    a.table[size_t(lo) * a.max_pages + a.n_pages[lo] + (rank - before)] = page;
+    a.refcount[page] = 1;
+  });
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.B; b += kThreads) {
+    const int need = upto[b] - (b > 0 ? upto[b - 1] : 0);
+    if (need > 0 && upto[b] <= served) a.n_pages[b] += need;
+  }
+}
+
+// -------------------------------------------------------------------- fork
+
+struct ForkJob {
+  int32_t from, to, rows, pad;   // rows == 0: nothing to copy
+};
+
+struct ForkArgs {
+  int32_t* table;           // [B, max_pages]
+  int32_t* n_pages;         // [B]
+  int32_t* refcount;        // [pool]
+  int32_t* length;          // [B]
+  const int32_t* src;       // [n]
+  const int32_t* dst;       // [n]
+  ForkJob* jobs;            // [n]
+  int B, n, max_pages, pool, page;
+};
+
+// One CTA, one thread per fork for the decisions, one warp per fork for the
+// rows of the table. Sources are never destinations of the same call, so no
+// row is read and written.
+__global__ void __launch_bounds__(kThreads) pages_fork_kernel(ForkArgs a) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  __shared__ int s_src[kMaxForks], s_dst[kMaxForks], s_fresh[kMaxForks], s_owner[kMaxForks];
+  __shared__ int part[kWarps];
+  const int i = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int src = -1, dst = -1, len = -1;
+  if (i < a.n) {
+    src = a.src[i];
+    dst = a.dst[i];
+  }
+  s_src[i] = src;
+  s_dst[i] = dst;
+  __syncthreads();
+  bool valid = i < a.n && src != -1;             // src -1: an unused entry
+  if (valid) {
+    int bad = 0;
+    if (src < 0 || src >= a.B || dst < 0 || dst >= a.B) {
+      bad = MD_DEV_BAD_ROW;
+    } else {
+      for (int j = 0; j < a.n; ++j)
+        if (s_src[j] == dst || (j < i && s_src[j] != -1 && s_dst[j] == dst)) bad = MD_DEV_BAD_ROW;
+      if (!bad) {
+        len = a.length[src];
+        const int hs = a.n_pages[src], hd = a.n_pages[dst];
+        if (hs < 0 || hs > a.max_pages || hd < 0 || hd > a.max_pages) bad = MD_DEV_BAD_PAGE;
+        else if (len > (long long)hs * a.page) bad = MD_DEV_BAD_PREFIX;
+      }
+    }
+    if (bad) {
+      set_status(bad);
+      valid = false;
+    }
+  }
+  const int full = valid && len > 0 ? len / a.page : 0;
+  const int rows = valid && len > 0 ? len % a.page : 0;
+  __syncthreads();
+  s_src[i] = valid ? src : -1;
+  s_fresh[i] = -1;
+  __syncthreads();
+  // the destinations' former pages go back first
+  for (int f = warp; f < a.n; f += kWarps) {
+    if (s_src[f] < 0) continue;
+    const int d = s_dst[f], held = a.n_pages[d];
+    for (int p = lane; p < held; p += 32) drop_page(a.refcount, a.pool, a.table[size_t(d) * a.max_pages + p]);
+  }
+  __syncthreads();
+  // a new page for every fork that ends inside one, lowest ids in list order
+  const int need = rows > 0 ? 1 : 0;
+  int total;
+  const int incl = block_incl_scan(need, part, total);
+  if (total > 0) {
+    if (need) s_owner[incl - 1] = i;
+    const int free_pages = count_free(a.refcount, a.pool, part);
+    if (total > free_pages && threadIdx.x == 0) set_status(MD_DEV_NO_PAGES);
+    take_lowest_free(a.refcount, a.pool, min(total, free_pages), part, [&](int rank, int page) {
+      s_fresh[s_owner[rank]] = page;
+      a.refcount[page] = 1;
+    });
+  }
+  __syncthreads();
+  const bool empty = !valid || len < 0 || (need && s_fresh[i] < 0);   // an idle source, or no page left
+  __shared__ int s_full[kMaxForks];
+  s_full[i] = empty ? -1 : full;
+  if (i < a.n) {
+    ForkJob job = {0, 0, 0, 0};
+    if (!empty && rows > 0) {
+      const int from = a.table[size_t(src) * a.max_pages + full];
+      if (from < 0 || from >= a.pool) set_status(MD_DEV_BAD_PAGE);
+      else job = {from, s_fresh[i], rows, 0};
+    }
+    a.jobs[i] = job;
+  }
+  __syncthreads();
+  for (int f = warp; f < a.n; f += kWarps) {
+    if (s_src[f] < 0) continue;
+    const int32_t* from = a.table + size_t(s_src[f]) * a.max_pages;
+    int32_t* to = a.table + size_t(s_dst[f]) * a.max_pages;
+    const int nf = s_full[f], held = a.n_pages[s_dst[f]];
+    const int last = max(max(nf, 0) + 1, held);  // entries past the former pages are -1 already
+    for (int p = lane; p < min(last, a.max_pages); p += 32) {
+      int page = -1;
+      if (p < nf) {
+        page = from[p];
+        if (page < 0 || page >= a.pool) set_status(MD_DEV_BAD_PAGE);
+        else atomicAdd(&a.refcount[page], 1);
+      } else if (p == nf) {
+        page = s_fresh[f];
+      }
+      to[p] = page;
+    }
+  }
+  __syncthreads();
+  if (valid) {
+    a.n_pages[dst] = empty ? 0 : full + need;
+    a.length[dst] = empty ? -1 : len;
+  }
+}
+
+// Copies the first `rows` slots of a fork's last page, every layer and head of
+// K and V. A head's slots of a page are contiguous: `rows` * dh elements.
+// One CTA per (layer and head, K or V, fork); traffic 4 * rows * dh B each.
+__global__ void __launch_bounds__(256) pages_fork_copy_kernel(uint4* k_pages, uint4* v_pages, const ForkJob* jobs, int pool,
+                                                              int Hkv, int page, int row16) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const ForkJob job = jobs[blockIdx.z];
+  if (job.rows == 0) return;
+  const int layer = blockIdx.x / Hkv, hk = blockIdx.x - layer * Hkv;
+  uint4* base = blockIdx.y ? v_pages : k_pages;
+  const uint4* from = base + ((size_t(layer) * pool + job.from) * Hkv + hk) * page * row16;
+  uint4* to = base + ((size_t(layer) * pool + job.to) * Hkv + hk) * page * row16;
+  const int n = job.rows * row16;
+  for (int i = threadIdx.x; i < n; i += 256) to[i] = from[i];
+}
+
+}  // namespace pages
+}  // namespace md
