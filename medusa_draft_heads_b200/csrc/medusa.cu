@@ -873,6 +873,119 @@ md_status launch_attn_tc(const AttnPlan& pl, const md_bf16* q, const md_bf16* kc
   return cuda_ok(cudaLaunchKernelEx(&cfg, attn_tc_kernel<DH, CH>, qmap, kmap, vmap, tree->tp, a));
 }
 
+// ------------------------ paged attention planning -------------------------
+
+template <int DH, bool F32>
+void paged_attn_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, dim3 grid, cudaStream_t st) {
+  *cfg = {};
+  cfg->gridDim = grid;
+  cfg->blockDim = dim3(md::attn_paged::kThreads);
+  cfg->dynamicSmemBytes = md::attn_paged::Cfg<DH>::kSmem;
+  cfg->stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = grid.x;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+}
+
+template <int DH, bool F32>
+md_status paged_attn_attributes() {
+  auto kern = md::attn_paged::attn_paged_kernel<DH, F32>;
+  md_status s = set_smem(kern, md::attn_paged::Cfg<DH>::kSmem);
+  if (s != MD_OK) return s;
+  return cuda_ok(cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+}
+
+// CTAs resident at once in clusters of `splits` on the current device.
+template <int DH, bool F32>
+int paged_attn_slots(int splits) {
+  static std::atomic<int> cache[kMaxDevices][md::attn_paged::kMaxSplits + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  int n = cache[dev][splits].load(std::memory_order_relaxed);
+  if (n == 0) {                          // stored as count + 1
+    int clusters = 0;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    paged_attn_config<DH, F32>(&cfg, attr, dim3(splits, 64), nullptr);
+    cfg.numAttrs = 1;
+    if (paged_attn_attributes<DH, F32>() != MD_OK ||
+        cudaOccupancyMaxActiveClusters(&clusters, md::attn_paged::attn_paged_kernel<DH, F32>, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      clusters = 0;
+    }
+    n = clusters * splits + 1;
+    cache[dev][splits].store(n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
+struct PagedAttnPlan {
+  int tpt, units, splits, sort;
+};
+
+// Row tiles hold whole nodes (G rows each); a unit is up to two tiles. The KV
+// splits are those that a count of waves finds shortest: every wave costs its
+// share of the chunks the table can hold, plus about three chunks' time for
+// the CTA's set-up, first loads and join (3 to 4 us against 1.1 us a chunk).
+PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, int max_pages, bool f32) {
+  PagedAttnPlan p;
+  const int G = Hq / Hkv;
+  p.tpt = md::attn_paged::kBM / G;
+  p.units = (T + 2 * p.tpt - 1) / (2 * p.tpt);
+  const int64_t base = int64_t(B) * Hkv * p.units;
+  const int chunks = int((int64_t(max_pages) * page + md::attn_paged::kBN - 1) / md::attn_paged::kBN);
+  double best = 0;
+  p.splits = 1;
+  p.sort = 0;
+  for (int s = 1; s <= md::attn_paged::kMaxSplits && s <= chunks; ++s) {
+    const int slots = dh == 128 ? (f32 ? paged_attn_slots<128, true>(s) : paged_attn_slots<128, false>(s))
+                                : (f32 ? paged_attn_slots<64, true>(s) : paged_attn_slots<64, false>(s));
+    if (slots < s) continue;
+    const int64_t waves = (base * s + slots - 1) / slots;
+    const double cost = double(waves) * (double((chunks + s - 1) / s) + 3.0);
+    if (best == 0 || cost < best) {
+      best = cost;
+      p.splits = s;
+      p.sort = B > 1 && waves > 1;
+    }
+  }
+  return p;
+}
+
+template <int DH, bool F32>
+md_status launch_attn_paged(const md::attn_paged::Args& a, const md_bf16* q, const md_bf16* k_pages,
+                            const md_tree* tree, cudaStream_t st) {
+  using namespace md::attn_paged;
+  md_status s;
+  CUtensorMap qmap, kmap, vmap;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return MD_ERR_CUDA;
+  {
+    // q [B*T][Hq][dh]: a box holds a tile's nodes, the G heads of one KV head each
+    cuuint64_t dims[3] = {cuuint64_t(DH), cuuint64_t(a.Hq), cuuint64_t(a.B) * tree->tp.T};
+    cuuint64_t strides[2] = {cuuint64_t(DH) * 2, cuuint64_t(a.Hq) * DH * 2};
+    cuuint32_t box[3] = {64, cuuint32_t(a.G), cuuint32_t(a.tpt)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    if (fn(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<md_bf16*>(q), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return MD_ERR_CUDA;
+  }
+  const uint64_t heads = uint64_t(a.pool) * a.Hkv;
+  if ((s = make_map_3d_sw128(&kmap, k_pages, DH, a.page, heads, 64, a.piece)) != MD_OK) return s;
+  if ((s = make_map_3d_sw128(&vmap, a.v_pages, DH, a.page, heads, 64, a.piece)) != MD_OK) return s;
+  if ((s = paged_attn_attributes<DH, F32>()) != MD_OK) return s;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  paged_attn_config<DH, F32>(&cfg, attr, dim3(a.splits, a.Hkv * a.units, a.B), st);
+  return cuda_ok(cudaLaunchKernelEx(&cfg, attn_paged_kernel<DH, F32>, qmap, kmap, vmap, tree->tp, a));
+}
+
 // ----------------------------- Hydra planning ------------------------------
 // Level l drafts the children of the depth-l nodes that have children: B * n[l]
 // head rows, top-k rows row0[l] + b * n[l] + slot[p] of one [rows, kmax] array.
@@ -1484,17 +1597,19 @@ md_status md_tree_attention_paged(const md_bf16* q, const md_bf16* k_pages, cons
     return MD_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16)) return MD_ERR_INVALID_ARG;
   if (!ws || ws_bytes < need || !aligned(ws, 256)) return MD_ERR_WORKSPACE;
+  const PagedAttnPlan pl = paged_attn_plan(B, tree->tp.T, Hq, Hkv, dh, page_size, max_pages, out_type == MD_OUT_F32);
   md::attn_paged::Args a;
-  a.q = q; a.kp = k_pages; a.vp = v_pages; a.table = block_table; a.prefix_len = prefix_len; a.out = out;
-  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.pool = pool_pages; a.page = page_size; a.max_pages = max_pages;
+  a.v_pages = v_pages; a.table = block_table; a.prefix_len = prefix_len; a.out = out;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.pool = pool_pages; a.page = page_size; a.max_pages = max_pages;
+  a.piece = std::min(page_size & -page_size, md::attn_paged::kBN);
+  a.tpt = pl.tpt; a.units = pl.units; a.splits = pl.splits; a.sort = pl.sort;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(float(dh))) * 1.4426950408889634f;
-  a.out_bf16 = out_type == MD_OUT_BF16;
-  const dim3 grid((tree->tp.T * Hq + 3) / 4, B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dh == 128 ? launch_pdl(md::attn_paged::attn_paged_rows_kernel<128>, grid, dim3(md::attn_paged::kThreads), 0, st,
-                                tree->tp, a)
-                   : launch_pdl(md::attn_paged::attn_paged_rows_kernel<64>, grid, dim3(md::attn_paged::kThreads), 0, st,
-                                tree->tp, a);
+  if (out_type == MD_OUT_F32)
+    return dh == 128 ? launch_attn_paged<128, true>(a, q, k_pages, tree, st)
+                     : launch_attn_paged<64, true>(a, q, k_pages, tree, st);
+  return dh == 128 ? launch_attn_paged<128, false>(a, q, k_pages, tree, st)
+                   : launch_attn_paged<64, false>(a, q, k_pages, tree, st);
 }
 
 md_status md_qk_rope_append(const md_bf16* q, const md_bf16* k, const md_bf16* v, const int64_t* strides,

@@ -8,9 +8,11 @@ from __future__ import annotations
 
 import torch
 
-from .binding import (Tree, accept_workspace_bytes, attention_workspace_bytes, heads_shared_workspace_bytes,
-                      heads_workspace_bytes, medusa_heads, medusa_heads_sampled, medusa_heads_shared, tree_accept,
-                      tree_accept_rejection, tree_accept_sampled, tree_attention, tree_build, tree_commit, workspace)
+from .binding import (Tree, accept_workspace_bytes, attention_paged_workspace_bytes, attention_workspace_bytes,
+                      heads_shared_workspace_bytes, heads_workspace_bytes, medusa_heads, medusa_heads_sampled,
+                      medusa_heads_shared, pages_fork, pages_fork_workspace_bytes, pages_resize, qk_rope_append,
+                      tree_accept, tree_accept_rejection, tree_accept_sampled, tree_attention, tree_attention_paged,
+                      tree_build, tree_commit, tree_commit_paged, workspace)
 from .tree_spec import tree_arrays
 
 
@@ -59,8 +61,11 @@ class MedusaStep:
         self.head_row = None
         ws_fn = heads_shared_workspace_bytes if shared_vocab else heads_workspace_bytes
         self.ws_heads = workspace(ws_fn(M, d, V, K, self.kmax), dev)
-        self.ws_attn = workspace(attention_workspace_bytes(B, self.T, Hq, Hkv, dh, S_max), dev)
+        self.ws_attn = workspace(self._attention_workspace_bytes(), dev)
         self.ws_acc = workspace(accept_workspace_bytes(B, self.T, V), dev)
+
+    def _attention_workspace_bytes(self):
+        return attention_workspace_bytes(self.B, self.T, self.Hq, self.Hkv, self.dh, self.S_max)
 
     def heads(self, h, W1, b1, Wv, stream=None):
         if self.mode == "rejection":
@@ -107,3 +112,75 @@ class MedusaStep:
         self.build(root_token, prefix_len, head_row, stream)
         self.attention(q, k_cache, v_cache, prefix_len, stream)
         self.accept(logits, stream)
+
+
+class PagedMedusaStep(MedusaStep):
+    """The step over a KV cache held in pages.
+
+    The caller owns the pools ([layers, pool_pages, Hkv, page_size, dh] bf16, K
+    and V); this object owns which request holds which page (`block_table`,
+    `n_pages`, `refcount`, all on the device) and the rotated queries `q` of the
+    layer at hand. A request is a row of the batch; prefix_len[b] = -1 marks a
+    row that holds none, so rows come and go without a change of shapes:
+
+        step.prefill_pages(length)                     # a new request's pages
+        step.append(q, k, v, pos, inv_freq, k_pages[i], v_pages[i], prefix_len, n_new=n)     # its prompt, layer i
+        step.heads(...); step.build(root_token, prefix_len)
+        step.reserve(prefix_len)                       # pages for the tree's T slots
+        step.append(q, k, v, step.pos, inv_freq, k_pages[i], v_pages[i], prefix_len)         # every layer i
+        step.attention(step.q, k_pages[i], v_pages[i], prefix_len)
+        step.accept(logits); step.commit(k_pages, v_pages, prefix_len)                       # all layers at once
+        step.trim()                                    # pages past the new prefixes go back
+    """
+
+    def __init__(self, *, page_size, max_pages, pool_pages, out_dtype=torch.float32, **kw):
+        self.page_size, self.max_pages = page_size, max_pages
+        super().__init__(S_max=page_size * max_pages, **kw)
+        dev = self.tokens.device
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.block_table = torch.full((self.B, max_pages), -1, **i32)
+        self.n_pages = torch.zeros((self.B,), **i32)
+        self.refcount = torch.zeros((pool_pages,), **i32)
+        self.attn_out = torch.empty((self.B, self.T, self.Hq, self.dh), dtype=out_dtype, device=dev)
+        self.q = torch.empty((self.B, self.T, self.Hq, self.dh), dtype=torch.bfloat16, device=dev)
+        self.ws_fork = None
+
+    def _attention_workspace_bytes(self):
+        return attention_paged_workspace_bytes(self.B, self.T, self.Hq, self.Hkv, self.dh, self.page_size, self.max_pages)
+
+    def prefill_pages(self, length, stream=None):
+        """Every row holds exactly the pages of length[b] slots (-1: none)."""
+        pages_resize(self.block_table, self.n_pages, self.refcount, length, self.page_size, stream=stream)
+
+    def reserve(self, prefix_len, stream=None):
+        """Pages for the prefix and the tree behind it."""
+        pages_resize(self.block_table, self.n_pages, self.refcount, prefix_len, self.page_size, extra=self.T,
+                     stream=stream)
+
+    def trim(self, stream=None):
+        """After commit: the pages past the new prefixes go back."""
+        self.prefill_pages(self.new_prefix_len, stream)
+
+    def append(self, q, k, v, pos, inv_freq, k_pages, v_pages, prefix_len, q_norm=None, k_norm=None, eps=1e-6,
+               interleaved=False, n_new=None, q_out=None, stream=None):
+        """Norms, rotation and cache write of one layer's new tokens; the queries
+        go to q_out (default: `self.q`, a tree's)."""
+        qk_rope_append(q, k, v, pos, inv_freq, self.q if q_out is None else q_out, k_pages, v_pages, self.block_table,
+                       prefix_len, q_norm=q_norm, k_norm=k_norm, eps=eps, interleaved=interleaved, n_new=n_new,
+                       stream=stream)
+
+    def attention(self, q, k_pages, v_pages, prefix_len, stream=None):
+        tree_attention_paged(q, k_pages, v_pages, self.block_table, prefix_len, self.tree, self.attn_out, self.ws_attn,
+                             stream=stream)
+
+    def commit(self, k_pages, v_pages, prefix_len, stream=None):
+        tree_commit_paged(k_pages, v_pages, self.block_table, self.tree, prefix_len, self.accept_len, self.path,
+                          self.bonus, self.new_prefix_len, self.next_root, self.next_head_row, stream=stream)
+
+    def fork(self, k_pages, v_pages, src, dst, prefix_len, stream=None):
+        """Rows dst continue the sequences of rows src; prefix_len[dst] is set."""
+        n = src.shape[0]
+        if self.ws_fork is None or self.ws_fork.numel() < pages_fork_workspace_bytes(self.B, n):
+            self.ws_fork = workspace(pages_fork_workspace_bytes(self.B, n), self.tokens.device)
+        pages_fork(k_pages, v_pages, self.block_table, self.n_pages, self.refcount, src, dst, prefix_len, self.ws_fork,
+                   stream=stream)
