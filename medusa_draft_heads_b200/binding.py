@@ -408,38 +408,68 @@ def tree_commit(k_cache, v_cache, tree: Tree, prefix_len, accept_len, path, bonu
 # The step over a paged KV cache.
 # ---------------------------------------------------------------------------
 
-class _on_device:
-    """Makes the device of a call's tensors current while it launches: checks
-    that all of them (None aside) live on one, and picks that device's current
+_I64x9 = ctypes.c_int64 * 9
+
+
+def _refuse(what, t, name, dtype, shape, dev):
+    """Raises for the first thing wrong with a tensor (_ptrs found something)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: {name}: expected a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: {name}: must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: {name}: must be contiguous")
+    raise ValueError(f"{what}: {name} is on cuda:{t.get_device()}, expected cuda:{dev}")
+
+
+def _ptrs(what, dev, *specs):
+    """Pointers of a call's dense tensors, (tensor, name, dtype, shape) each, all on
+    device `dev`. A step makes a call per layer, so the checks are few attribute
+    reads; _refuse finds the words for one that fails."""
+    out = []
+    for t, name, dtype, shape in specs:
+        try:
+            ok = t.dtype is dtype and t.get_device() == dev >= 0 and t.shape == shape and t.is_contiguous()
+        except AttributeError:
+            ok = False
+        if not ok:
+            _refuse(what, t, name, dtype, shape, dev)
+        out.append(t.data_ptr())
+    return out
+
+
+def _dims(what, t, name, n):
+    """The shape of a tensor with n dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: {name}: expected a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{what}: {name}: expected {n} dims, got {t.dim()}")
+    return t.shape
+
+
+def _pool_dims(what, t):
+    """(layers, pool_pages, Hkv, page_size, dh) of a pool of one layer or of a stack."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: k_pages: expected a torch.Tensor")
+    if t.dim() not in (4, 5):
+        raise ValueError(f"{what}: k_pages: expected 4 or 5 dims, got {t.dim()}")
+    return tuple(t.shape) if t.dim() == 5 else (1, *t.shape)
+
+
+def _launch(what, fn, dev, stream, *args):
+    """Calls fn with the device of its tensors current, on that device's current
     stream unless the caller gave one."""
-
-    def __init__(self, what, stream, **tensors):
-        devs = {name: t.device for name, t in tensors.items() if isinstance(t, torch.Tensor)}
-        first = next(iter(devs.values()))
-        for name, d in devs.items():
-            if d != first:
-                raise ValueError(f"{what}: {name} is on {d}, expected {first}")
-        self.device, self.stream = first, stream
-
-    def __enter__(self):
-        self.guard = torch.cuda.device(self.device)
-        self.guard.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream if self.stream is None else _stream(self.stream)
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
-
-
-def _pools(what, k_pages, v_pages, layered):
-    """(layers, pool_pages, Hkv, page_size, dh) of a pair of pools."""
-    dims = (4, 5) if layered else (4,)
-    if k_pages.dim() not in dims:
-        raise ValueError(f"{what}: k_pages has {k_pages.dim()} dims, expected "
-                         + ("[pages, Hkv, page_size, dh] or [layers, pages, Hkv, page_size, dh]" if layered
-                            else "[pages, Hkv, page_size, dh]"))
-    _same(what, v_pages=(tuple(v_pages.shape), tuple(k_pages.shape)))
-    shape = tuple(k_pages.shape)
-    return shape if len(shape) == 5 else (1,) + shape
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream))
+    if rc != 0:
+        _check(rc, what)
 
 
 def attention_paged_workspace_bytes(B, T, Hq, Hkv, dh, page_size, max_pages) -> int:
@@ -452,40 +482,42 @@ def attention_paged_workspace_bytes(B, T, Hq, Hkv, dh, page_size, max_pages) -> 
 def tree_attention_paged(q, k_pages, v_pages, block_table, prefix_len, tree: Tree, out, ws, scale=0.0, stream=None):
     """md_tree_attention_paged: q [B,T,Hq,dh], pools [pages,Hkv,page_size,dh] bf16, block_table
     [B,max_pages] int32 -> out [B,T,Hq,dh], fp32 or bf16 (by its dtype). prefix_len -1: an idle slot."""
-    B, T, Hq, dh = q.shape
-    _, pages, Hkv, page, dhk = _pools("tree_attention_paged", k_pages, v_pages, layered=False)
-    _same("tree_attention_paged", T=(T, tree.T), k_pages_dh=(dhk, dh), block_table_rows=(block_table.shape[0], B),
-          prefix_len=(tuple(prefix_len.shape), (B,)), out=(tuple(out.shape), (B, T, Hq, dh)))
-    if out.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"out: expected torch.float32 or torch.bfloat16, got {out.dtype}")
-    args = (_ptr(q, torch.bfloat16, "q", 4), _ptr(k_pages, torch.bfloat16, "k_pages", 4),
-            _ptr(v_pages, torch.bfloat16, "v_pages", 4), pages, page, _ptr(block_table, torch.int32, "block_table", 2),
-            block_table.shape[1], _ptr(prefix_len, torch.int32, "prefix_len"), tree.handle, B, Hq, Hkv, dh, float(scale),
-            _ptr(out, out.dtype, "out", 4), MD_OUT_BF16 if out.dtype == torch.bfloat16 else MD_OUT_F32,
-            _ptr(ws, torch.uint8, "ws"), ws.numel())
-    with _on_device("tree_attention_paged", stream, q=q, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
-                    prefix_len=prefix_len, out=out, ws=ws) as st:
-        rc = lib().md_tree_attention_paged(*args, st)
-    _check(rc, "md_tree_attention_paged")
+    what = "tree_attention_paged"
+    B, T, Hq, dh = _dims(what, q, "q", 4)
+    pages, Hkv, page, _ = _dims(what, k_pages, "k_pages", 4)
+    width = _dims(what, block_table, "block_table", 2)[1]
+    if T != tree.T:
+        raise ValueError(f"{what}: T has shape {T}, expected {tree.T}")
+    out_dtype = getattr(out, "dtype", None)
+    if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
+        raise TypeError(f"{what}: out: expected torch.float32 or torch.bfloat16, got {out_dtype}")
+    dev = q.get_device()
+    pool = (pages, Hkv, page, dh)
+    qp, kp, vp, tp, lp, op, wp = _ptrs(
+        what, dev, (q, "q", torch.bfloat16, q.shape), (k_pages, "k_pages", torch.bfloat16, pool),
+        (v_pages, "v_pages", torch.bfloat16, pool), (block_table, "block_table", torch.int32, (B, width)),
+        (prefix_len, "prefix_len", torch.int32, (B,)), (out, "out", out_dtype, q.shape),
+        (ws, "ws", torch.uint8, getattr(ws, "shape", ())))
+    _launch("md_tree_attention_paged", lib().md_tree_attention_paged, dev, stream, qp, kp, vp, pages, page, tp, width, lp,
+            tree.handle, B, Hq, Hkv, dh, scale, op, MD_OUT_BF16 if out_dtype is torch.bfloat16 else MD_OUT_F32, wp,
+            ws.numel())
 
 
-def _head_rows(t, name, B, T, H, dh):
+def _head_rows(what, t, name, dev, shape):
     """Pointer and element strides (request, token, head) of a [B,T,H,dh] view
     whose last dimension is contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    _same("qk_rope_append", **{name: (tuple(t.shape), (B, T, H, dh))})
-    if t.stride(3) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev or dev < 0:
+        _refuse(what, t, name, torch.bfloat16, shape, dev)
+    sb, st, sh, sd = t.stride()
+    B, T, H, _ = shape
     # a dimension of size 1 is never stepped over: its stride may be anything
-    strides = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
-    if any(s % 8 for s in strides) or t.data_ptr() % 16:
-        raise ValueError(f"{name}: rows must start on 16-byte boundaries")
-    return t.data_ptr(), strides
+    sb, st, sh = sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0
+    p = t.data_ptr()
+    if sd != 1:
+        raise ValueError(f"{what}: {name}: the last dimension must be contiguous")
+    if (sb | st | sh) % 8 or p % 16:
+        raise ValueError(f"{what}: {name}: rows must start on 16-byte boundaries")
+    return p, sb, st, sh
 
 
 def qk_rope_append(q, k, v, pos, inv_freq, q_out, k_pages, v_pages, block_table, prefix_len, q_norm=None, k_norm=None,
@@ -494,71 +526,63 @@ def qk_rope_append(q, k, v, pos, inv_freq, q_out, k_pages, v_pages, block_table,
     pos [B,T] * inv_freq [rot/2] of q [B,T,Hq,dh] into q_out (dense) and of k [B,T,Hkv,dh] into
     slots prefix_len[b] + t of the pools, v beside it. q, k, v: bf16 views (of one fused
     projection, say). n_new [B]: tokens of each request (the rest of T is padding)."""
-    B, T, Hq, dh = q.shape
-    Hkv = k.shape[2]
-    _, pages, hk, page, dhk = _pools("qk_rope_append", k_pages, v_pages, layered=False)
-    _same("qk_rope_append", k_pages=((hk, dhk), (Hkv, dh)), pos=(tuple(pos.shape), (B, T)),
-          q_out=(tuple(q_out.shape), (B, T, Hq, dh)), block_table_rows=(block_table.shape[0], B),
-          prefix_len=(tuple(prefix_len.shape), (B,)))
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None:
-            _same("qk_rope_append", **{name: (tuple(w.shape), (dh,))})
+    what = "qk_rope_append"
+    B, T, Hq, dh = shape = _dims(what, q, "q", 4)
+    Hkv = _dims(what, k, "k", 4)[2]
+    pages, _, page, _ = _dims(what, k_pages, "k_pages", 4)
+    width = _dims(what, block_table, "block_table", 2)[1]
+    half = _dims(what, inv_freq, "inv_freq", 1)[0]
+    dev = q.get_device()
+    pool, kshape = (pages, Hkv, page, dh), (B, T, Hkv, dh)
+    qp, *qs = _head_rows(what, q, "q", dev, shape)
+    kp, *ks = _head_rows(what, k, "k", dev, kshape)
+    vp, *vs = _head_rows(what, v, "v", dev, kshape)
+    pp, fp, op, kpp, vpp, tp, lp = _ptrs(
+        what, dev, (pos, "pos", torch.int32, (B, T)), (inv_freq, "inv_freq", torch.float32, (half,)),
+        (q_out, "q_out", torch.bfloat16, shape), (k_pages, "k_pages", torch.bfloat16, pool),
+        (v_pages, "v_pages", torch.bfloat16, pool), (block_table, "block_table", torch.int32, (B, width)),
+        (prefix_len, "prefix_len", torch.int32, (B,)))
+    qn = kn = np_ = None
+    if q_norm is not None:
+        qn, = _ptrs(what, dev, (q_norm, "q_norm", torch.bfloat16, (dh,)))
+    if k_norm is not None:
+        kn, = _ptrs(what, dev, (k_norm, "k_norm", torch.bfloat16, (dh,)))
     if n_new is not None:
-        _same("qk_rope_append", n_new=(tuple(n_new.shape), (B,)))
-    qp, qs = _head_rows(q, "q", B, T, Hq, dh)
-    kp, ks = _head_rows(k, "k", B, T, Hkv, dh)
-    vp, vs = _head_rows(v, "v", B, T, Hkv, dh)
-    strides = (ctypes.c_int64 * 9)(*qs, *ks, *vs)
-    args = (qp, kp, vp, strides, _ptr(pos, torch.int32, "pos"), _ptr(inv_freq, torch.float32, "inv_freq", 1),
-            2 * inv_freq.shape[0], int(bool(interleaved)), _ptr(q_norm, torch.bfloat16, "q_norm"),
-            _ptr(k_norm, torch.bfloat16, "k_norm"), float(eps), _ptr(q_out, torch.bfloat16, "q_out"),
-            _ptr(k_pages, torch.bfloat16, "k_pages"), _ptr(v_pages, torch.bfloat16, "v_pages"), pages, page,
-            _ptr(block_table, torch.int32, "block_table", 2), block_table.shape[1],
-            _ptr(prefix_len, torch.int32, "prefix_len"), _ptr(n_new, torch.int32, "n_new"), B, T, Hq, Hkv, dh)
-    with _on_device("qk_rope_append", stream, q=q, k=k, v=v, pos=pos, inv_freq=inv_freq, q_out=q_out, k_pages=k_pages,
-                    v_pages=v_pages, block_table=block_table, prefix_len=prefix_len, q_norm=q_norm, k_norm=k_norm,
-                    n_new=n_new) as st:
-        rc = lib().md_qk_rope_append(*args, st)
-    _check(rc, "md_qk_rope_append")
+        np_, = _ptrs(what, dev, (n_new, "n_new", torch.int32, (B,)))
+    _launch("md_qk_rope_append", lib().md_qk_rope_append, dev, stream, qp, kp, vp, _I64x9(*qs, *ks, *vs), pp, fp, 2 * half,
+            1 if interleaved else 0, qn, kn, eps, op, kpp, vpp, pages, page, tp, width, lp, np_, B, T, Hq, Hkv, dh)
 
 
 def tree_commit_paged(k_pages, v_pages, block_table, tree: Tree, prefix_len, accept_len, path, bonus, new_prefix_len,
                       next_root, next_head_row, stream=None):
     """md_tree_commit_paged: tree_commit over pools [pages,Hkv,page_size,dh], or
     [layers,pages,Hkv,page_size,dh] for every layer at once (in place)."""
-    B = block_table.shape[0]
-    layers, pages, Hkv, page, dh = _pools("tree_commit_paged", k_pages, v_pages, layered=True)
-    K = path.shape[1] - 1
-    _same("tree_commit_paged", path_rows=(path.shape[0], B), prefix_len=(tuple(prefix_len.shape), (B,)),
-          accept_len=(tuple(accept_len.shape), (B,)), bonus=(tuple(bonus.shape), (B,)),
-          new_prefix_len=(tuple(new_prefix_len.shape), (B,)), next_root=(tuple(next_root.shape), (B,)),
-          next_head_row=(tuple(next_head_row.shape), (B,)))
-    args = (_ptr(k_pages, torch.bfloat16, "k_pages"), _ptr(v_pages, torch.bfloat16, "v_pages"), layers, pages, page,
-            _ptr(block_table, torch.int32, "block_table", 2), block_table.shape[1], Hkv, dh, tree.handle, B,
-            _ptr(prefix_len, torch.int32, "prefix_len"), _ptr(accept_len, torch.int32, "accept_len"),
-            _ptr(path, torch.int32, "path", 2), K, _ptr(bonus, torch.int32, "bonus"),
-            _ptr(new_prefix_len, torch.int32, "new_prefix_len"), _ptr(next_root, torch.int32, "next_root"),
-            _ptr(next_head_row, torch.int32, "next_head_row"))
-    with _on_device("tree_commit_paged", stream, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
-                    prefix_len=prefix_len, accept_len=accept_len, path=path, bonus=bonus, new_prefix_len=new_prefix_len,
-                    next_root=next_root, next_head_row=next_head_row) as st:
-        rc = lib().md_tree_commit_paged(*args, st)
-    _check(rc, "md_tree_commit_paged")
+    what = "tree_commit_paged"
+    layers, pages, Hkv, page, dh = _pool_dims(what, k_pages)
+    B, width = _dims(what, block_table, "block_table", 2)
+    cols = _dims(what, path, "path", 2)[1]
+    dev, i32, rows = k_pages.get_device(), torch.int32, (B,)
+    kp, vp, tp, lp, ap, pp, bp, np_, rp, hp = _ptrs(
+        what, dev, (k_pages, "k_pages", torch.bfloat16, k_pages.shape), (v_pages, "v_pages", torch.bfloat16, k_pages.shape),
+        (block_table, "block_table", i32, (B, width)), (prefix_len, "prefix_len", i32, rows),
+        (accept_len, "accept_len", i32, rows), (path, "path", i32, (B, cols)), (bonus, "bonus", i32, rows),
+        (new_prefix_len, "new_prefix_len", i32, rows), (next_root, "next_root", i32, rows),
+        (next_head_row, "next_head_row", i32, rows))
+    _launch("md_tree_commit_paged", lib().md_tree_commit_paged, dev, stream, kp, vp, layers, pages, page, tp, width, Hkv, dh,
+            tree.handle, B, lp, ap, pp, cols - 1, bp, np_, rp, hp)
 
 
 def pages_resize(block_table, n_pages, refcount, length, page_size, extra=0, stream=None):
     """md_pages_resize: rows of block_table [B,max_pages] grow (lowest free pages of refcount
     [pages] in row order) or shrink to ceil((length + extra) / page_size) pages, in place.
     length [B]; -1 frees the row."""
-    B, width = block_table.shape
-    _same("pages_resize", n_pages=(tuple(n_pages.shape), (B,)), length=(tuple(length.shape), (B,)))
-    args = (_ptr(block_table, torch.int32, "block_table", 2), _ptr(n_pages, torch.int32, "n_pages"),
-            _ptr(refcount, torch.int32, "refcount", 1), _ptr(length, torch.int32, "length"), B, width, refcount.shape[0],
-            int(page_size), int(extra))
-    with _on_device("pages_resize", stream, block_table=block_table, n_pages=n_pages, refcount=refcount,
-                    length=length) as st:
-        rc = lib().md_pages_resize(*args, st)
-    _check(rc, "md_pages_resize")
+    what = "pages_resize"
+    B, width = _dims(what, block_table, "block_table", 2)
+    pages = _dims(what, refcount, "refcount", 1)[0]
+    dev, i32 = block_table.get_device(), torch.int32
+    tp, np_, rp, lp = _ptrs(what, dev, (block_table, "block_table", i32, (B, width)), (n_pages, "n_pages", i32, (B,)),
+                            (refcount, "refcount", i32, (pages,)), (length, "length", i32, (B,)))
+    _launch("md_pages_resize", lib().md_pages_resize, dev, stream, tp, np_, rp, lp, B, width, pages, page_size, extra)
 
 
 def pages_fork_workspace_bytes(B, n) -> int:
@@ -571,19 +595,18 @@ def pages_fork(k_pages, v_pages, block_table, n_pages, refcount, src, dst, lengt
     """md_pages_fork: row dst[i] of the table becomes a copy of row src[i]: full pages shared, the
     last, partly filled one copied in every layer of the pools ([pages,Hkv,page_size,dh] or
     [layers,...]). length [B] is updated; src[i] = -1 is an unused entry."""
-    B, width = block_table.shape
-    layers, pages, Hkv, page, dh = _pools("pages_fork", k_pages, v_pages, layered=True)
-    _same("pages_fork", n_pages=(tuple(n_pages.shape), (B,)), length=(tuple(length.shape), (B,)),
-          refcount=(tuple(refcount.shape), (pages,)), dst=(tuple(dst.shape), (src.shape[0],)))
-    args = (_ptr(k_pages, torch.bfloat16, "k_pages"), _ptr(v_pages, torch.bfloat16, "v_pages"), layers, pages, Hkv, page,
-            dh, _ptr(block_table, torch.int32, "block_table", 2), _ptr(n_pages, torch.int32, "n_pages"),
-            _ptr(refcount, torch.int32, "refcount", 1), _ptr(length, torch.int32, "length"), B, width,
-            _ptr(src, torch.int32, "src", 1), _ptr(dst, torch.int32, "dst", 1), src.shape[0],
-            _ptr(ws, torch.uint8, "ws"), ws.numel())
-    with _on_device("pages_fork", stream, k_pages=k_pages, v_pages=v_pages, block_table=block_table, n_pages=n_pages,
-                    refcount=refcount, src=src, dst=dst, length=length, ws=ws) as st:
-        rc = lib().md_pages_fork(*args, st)
-    _check(rc, "md_pages_fork")
+    what = "pages_fork"
+    layers, pages, Hkv, page, dh = _pool_dims(what, k_pages)
+    B, width = _dims(what, block_table, "block_table", 2)
+    n = _dims(what, src, "src", 1)[0]
+    dev, i32 = k_pages.get_device(), torch.int32
+    kp, vp, tp, np_, rp, sp, dp, lp, wp = _ptrs(
+        what, dev, (k_pages, "k_pages", torch.bfloat16, k_pages.shape), (v_pages, "v_pages", torch.bfloat16, k_pages.shape),
+        (block_table, "block_table", i32, (B, width)), (n_pages, "n_pages", i32, (B,)),
+        (refcount, "refcount", i32, (pages,)), (src, "src", i32, (n,)), (dst, "dst", i32, (n,)),
+        (length, "length", i32, (B,)), (ws, "ws", torch.uint8, getattr(ws, "shape", ())))
+    _launch("md_pages_fork", lib().md_pages_fork, dev, stream, kp, vp, layers, pages, Hkv, page, dh, tp, np_, rp, lp, B,
+            width, sp, dp, n, wp, ws.numel())
 
 
 def device_status(clear: bool = True, stream=None) -> int:

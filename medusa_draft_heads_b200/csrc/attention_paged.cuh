@@ -53,24 +53,30 @@ namespace md {
 namespace attn_paged {
 
 constexpr int kBM = 128;              // rows of a tile
-constexpr int kBN = 128;              // keys of a chunk
-constexpr int kThreads = 384;
-constexpr int kSoftThreads = 256;
+constexpr int kBN = 128;              // keys of a chunk (a slot of the rings)
+constexpr int kSub = 64;              // keys of a job: half a chunk
+constexpr int kThreads = 640;
+constexpr int kSoftThreads = 512;
 constexpr int kKStages = 3;
 constexpr int kVStages = 3;           // the third only with one row tile
 constexpr int kMaxSplits = 16;        // CTAs of a cluster (above 8 by opt-in)
 constexpr float kRescaleLog2 = 8.0f;
 constexpr uint32_t kTmemCols = 512;   // S0, S1, O0, O1: 128 columns each
 
-template <int DH>
+template <int DH, bool F32>
 struct Cfg {
+  // bf16 results: two S buffers a stream, so that the next scores are ready when a
+  // job ends; fp32 ones: the three parts of P take the columns of the second
+  static constexpr int kBufs = F32 ? 1 : 2;
+  static constexpr int kParts = F32 ? 3 : 1;               // bf16 parts of P
   static constexpr int KB = DH / 64;                       // 64-column blocks
-  static constexpr uint32_t kTile = KB * 128 * 128;        // 128 rows x DH bf16, 128-byte swizzle
+  static constexpr uint32_t kQTile = KB * kBM * 128;       // 128 rows x DH bf16, 128-byte swizzle
+  static constexpr uint32_t kTile = KB * kBN * 128;        // a chunk of K or V
   static constexpr int kLd = DH + 4;                       // padded fp32 row of the staged O
   // Q0, Q1 (or a V slot), 3 K slots, 2 V slots
-  static constexpr uint32_t kRing = 7 * kTile;
-  static constexpr int kSmem = int(kRing) + 512 + 1024;    // + barriers, alignment
-  static_assert(2 * kBM * (kLd * 4 + 8) <= int(kRing), "staged O, (m, sum)");
+  static constexpr uint32_t kRing = 2 * kQTile + 5 * kTile;
+  static constexpr int kSmem = int(kRing) + 512 + 2048;    // + barriers, row maxima
+  static_assert(2 * kBM * (kLd * 4 + 8) + (2 * kBM + 2 * kMaxSplits) * 12 <= int(kRing), "staged O, (m, sum), weights");
 };
 
 struct Args {
@@ -81,9 +87,35 @@ struct Args {
   int B, Hq, Hkv, G, pool, page, max_pages;
   int piece;                   // rows of a TMA copy: the largest power of two dividing page, at most 128
   int tpt;                     // tree nodes of a row tile
+  int tpu;                     // row tiles of a unit: 1 or 2
   int units, splits, sort;
   float scale_log2;
 };
+
+// Two fp32 in one 64-bit register: the packed FMA and add of sm_100.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(f32x2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// NaN if one of them is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 __device__ __forceinline__ float exp2_sfu(float x) {
   float y;
@@ -105,6 +137,71 @@ __device__ __forceinline__ void settle(float* v) {
   asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
 
+// 16 columns, loaded and stored (few registers beside a row of scores).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]) : "memory");
+}
+
+// The MMAs and commits of attention_paged, issued by one elected lane of a
+// converged warp. The election sits inside the instruction's own predicate: code
+// around it stays convergent, so operands are computed and kept in uniform
+// registers, which is where an MMA takes them from (under a lane's branch each
+// operand of each MMA is moved there on its own: 80 clocks an MMA).
+__device__ __forceinline__ void umma_f16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_tmem_a_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                      uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+// mbar_wait, for waits that are short and many: the bounded form's clock and limit
+// (a timer and a global load) are only read once the phase is really late.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity);
+}
+
+__device__ __forceinline__ f32x2 exp2_sfu2(f32x2 x) {
+  float a, b;
+  unpair(x, a, b);
+  return pair(exp2_sfu(a), exp2_sfu(b));
+}
+
+// An fp32's leading 16 bits as a value, and those of two packed as bf16x2.
+__device__ __forceinline__ float high_part(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t high_halves(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+
+template <int N>
+struct IntTag {
+  static constexpr int value = N;
+};
+
 // Visibility of the 64 keys n0 .. n0 + 63 (n = slot - P) as bit j: prefix keys
 // (n < 0) always, tree node n iff it is in the row's ancestor set.
 __device__ __forceinline__ uint64_t visible_bits(uint64_t lo, uint64_t hi, int n0) {
@@ -121,10 +218,10 @@ __device__ __forceinline__ bool bf16_finite(uint32_t v) { return (v & 0x7F80u) !
 
 // The copies of one chunk of K or V into a ring slot, each lane a page piece.
 // Pieces behind the last slot are not copied. All lanes of a warp call it.
-template <int DH>
+template <int DH, bool F32>
 __device__ __forceinline__ void load_chunk(uint32_t dst, const CUtensorMap* map, uint32_t bar, const int32_t* row, int key0,
                                            int nkeys, int hk, const Args& a) {
-  using C = Cfg<DH>;
+  using C = Cfg<DH, F32>;
   const int lane = threadIdx.x & 31;
   const int left = min(kBN, nkeys - key0);
   const int pieces = (left + a.piece - 1) / a.piece;
@@ -148,11 +245,10 @@ template <int DH, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeParams tp, Args a) {
-  using C = Cfg<DH>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  using C = Cfg<DH, F32>;
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;                                    // 2 tiles (the second may be V slot 2)
-  uint8_t* sK = smem + 2 * C::kTile;                     // 3 slots
+  uint8_t* sK = smem + 2 * C::kQTile;                    // 3 slots
   uint8_t* sV = sK + kKStages * C::kTile;                // 2 slots
   float2* sML = reinterpret_cast<float2*>(smem + 2 * kBM * C::kLd * 4);   // [2][128], behind the staged O
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing);
@@ -161,31 +257,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_empty = k_full + kKStages;  // 3
   uint64_t* v_full = k_empty + kKStages;  // 3
   uint64_t* v_empty = v_full + kVStages;  // 3
-  uint64_t* s_full = v_empty + kVStages;  // 2
-  uint64_t* p_full = s_full + 2;          // 2
-  uint64_t* mma_done = p_full + 2;        // 1
+  uint64_t* s_full = v_empty + kVStages;  // [2 streams][2 buffers]
+  uint64_t* p_full = s_full + 4;          // [2][2]
+  uint64_t* o_full = p_full + 4;          // [2]
+  uint64_t* v_fixed = o_full + 2;         // [2]: the chunks that reach the tree, behind the V warp's look
+  uint64_t* mma_done = v_fixed + 2;       // 1
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   int* req = reinterpret_cast<int*>(tmem_slot + 1);
   int* bad_v = req + 1;
+  float* s_part = reinterpret_cast<float*>(smem + C::kRing + 512);        // [2 streams][2 halves][128]: row maxima, sums
 
   const int split = blockIdx.x, unit = blockIdx.y % a.units, hk = blockIdx.y / a.units;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __reduce_max_sync(0xffffffffu, int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int T = tp.T;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(q_full), 1);
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(smem_u32(&k_full[i]), 1);
-      mbar_init(smem_u32(&k_empty[i]), 1);
+      mbar_init(smem_u32(&k_empty[i]), 2);               // both streams
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(smem_u32(&v_full[i]), 1);
-      mbar_init(smem_u32(&v_empty[i]), 1);
+      mbar_init(smem_u32(&v_empty[i]), 2);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), 8);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 4);
+      mbar_init(smem_u32(&o_full[i]), 1);
+      mbar_init(smem_u32(&v_fixed[i]), 1);
     }
-    mbar_init(smem_u32(mma_done), 1);
+    mbar_init(smem_u32(mma_done), 2);
     fence_barrier_init();
     *req = blockIdx.z;
     *bad_v = 0;
@@ -193,6 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
+  }
+  if (lane == 0) {
+    if (warp == 0) prefetch_tensormap(&kmap);
+    if (warp == 2) prefetch_tensormap(&vmap);
+    if (warp == 3) prefetch_tensormap(&qmap);
   }
   pdl_wait_primary();          // inputs may come from earlier kernels
   pdl_launch_dependents();
@@ -220,14 +328,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (bad && P != -1 && split == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(MD_DEV_BAD_PREFIX);
   const int nkeys = bad ? 0 : P + T;
   const int nch_all = (nkeys + kBN - 1) / kBN;
-  const int c_begin = int((long long)nch_all * split / a.splits);
-  const int nch = int((long long)nch_all * (split + 1) / a.splits) - c_begin;
-  const int tok0 = unit * 2 * a.tpt;                   // nodes of this unit
-  const bool two = T - tok0 > a.tpt;                   // two row tiles
+  // at most 2^24 chunks and 16 splits
+  const int c_begin = int(uint32_t(nch_all) * uint32_t(split) / uint32_t(a.splits));
+  const int nch = int(uint32_t(nch_all) * uint32_t(split + 1) / uint32_t(a.splits)) - c_begin;
+  // jobs' keys: halves of chunks, without a last half that is all behind the keys
+  const int nsub = nch == 0 ? 0 : (min(nkeys, (c_begin + nch) * kBN) - c_begin * kBN + kSub - 1) / kSub;
+  const int tok0 = unit * a.tpu * a.tpt;               // nodes of this unit
+  const bool two = a.tpu == 2 && T - tok0 > a.tpt;     // two row tiles
   const int vst = two ? 2 : 3;                         // V slots in use
+  const int c_tree = max(0, (P - c_begin * kBN) / kBN);   // first chunk with tree slots (at most two have any), if below nch
   const int32_t* trow = a.table + size_t(b) * a.max_pages;
-  auto v_slot = [&](int s) -> uint8_t* { return s < 2 ? sV + s * C::kTile : sQ + C::kTile; };
+  auto v_slot = [&](int s) -> uint8_t* { return s < 2 ? sV + s * C::kTile : sQ + C::kQTile; };
 
+  if (warp < 4) {
   if (warp == 0) {
     // ------------------------------------ K ------------------------------------
     bool ok = true;
@@ -236,15 +349,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < nch; ++c) {
       if (c == withhold) continue;
       const int st = c % kKStages;
-      if (c >= kKStages && !mbar_wait(smem_u32(&k_empty[st]), ((c / kKStages) - 1) & 1)) ok = false;
+      if (c >= kKStages && !wait_phase(smem_u32(&k_empty[st]), ((c / kKStages) - 1) & 1)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      load_chunk<DH>(smem_u32(sK + st * C::kTile), &kmap, smem_u32(&k_full[st]), trow, (c_begin + c) * kBN, nkeys, hk, a);
+      load_chunk<DH, F32>(smem_u32(sK + st * C::kTile), &kmap, smem_u32(&k_full[st]), trow, (c_begin + c) * kBN, nkeys, hk, a);
       n = c + 1;
     }
     // every copy issued into this CTA's shared memory lands before it may exit
     for (int c = (n > kKStages ? n - kKStages : 0); c < n; ++c)
-      if (c != withhold) ok = mbar_wait(smem_u32(&k_full[c % kKStages]), (c / kKStages) & 1) && ok;
+      if (c != withhold) ok = wait_phase(smem_u32(&k_full[c % kKStages]), (c / kKStages) & 1) && ok;
     if (!ok && lane == 0) set_status(MD_DEV_TIMEOUT);
   } else if (warp == 2) {
     // ------------------------------------ V ------------------------------------
@@ -254,84 +367,150 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < nch; ++c) {
       if (c == withhold) continue;
       const int st = c % vst;
-      if (c >= vst && !mbar_wait(smem_u32(&v_empty[st]), ((c / vst) - 1) & 1)) ok = false;
+      if (c >= vst && !wait_phase(smem_u32(&v_empty[st]), ((c / vst) - 1) & 1)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      load_chunk<DH>(smem_u32(v_slot(st)), &vmap, smem_u32(&v_full[st]), trow, (c_begin + c) * kBN, nkeys, hk, a);
+      load_chunk<DH, F32>(smem_u32(v_slot(st)), &vmap, smem_u32(&v_full[st]), trow, (c_begin + c) * kBN, nkeys, hk, a);
       n = c + 1;
     }
-    for (int c = (n > vst ? n - vst : 0); c < n; ++c)
-      if (c != withhold) ok = mbar_wait(smem_u32(&v_full[c % vst]), (c / vst) & 1) && ok;
-    if (!ok && lane == 0) set_status(MD_DEV_TIMEOUT);
-  } else if (warp == 3) {
-    // ------------------------------------ Q ------------------------------------
-    if (lane == 0 && nch > 0) {
-      const uint32_t qb = smem_u32(q_full);
-      const int tiles = two ? 2 : 1;
-      mbar_arrive_expect_tx(qb, uint32_t(tiles * a.tpt * a.G) * DH * 2);
-      for (int w = 0; w < tiles; ++w)
+    // V rows that P's zeros must not meet: slots behind the last key, and what is
+    // not finite in the tree's (a node may not reach the rows that do not see it)
+    for (int c = c_tree; c < nch && ok; ++c) {
+      ok = __all_sync(0xffffffffu, c != withhold && wait_phase(smem_u32(&v_full[c % vst]), (c / vst) & 1));
+      if (!ok) break;
+      const int key0 = (c_begin + c) * kBN, valid = min(kBN, nkeys - key0);
+      const int first = T > 1 ? max(0, P - key0) : valid;
+      bool fixed = false;
+      for (int kb = 0; kb < C::KB; ++kb) {
+        uint4* v = reinterpret_cast<uint4*>(v_slot(c % vst) + kb * (kBN * 128));   // 8 pieces of 16 bytes a row
+#pragma unroll 4
+        for (int i = first * 8 + lane; i < valid * 8; i += 32) {
+          uint4 x = v[i];
+          uint32_t h[4] = {x.x, x.y, x.z, x.w};
+          bool fix = false;
 #pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb)
-          tma_load_3d(smem_u32(sQ + w * C::kTile + kb * (kBM * 128)), &qmap, kb * 64, hk * a.G,
-                      b * T + tok0 + w * a.tpt, qb);
-      if (!mbar_wait(qb, 0)) set_status(MD_DEV_TIMEOUT);
+          for (int e = 0; e < 4; ++e) {
+            if (!bf16_finite(h[e])) { h[e] &= 0xFFFF0000u; fix = true; }
+            if (!bf16_finite(h[e] >> 16)) { h[e] &= 0x0000FFFFu; fix = true; }
+          }
+          if (fix) v[i] = make_uint4(h[0], h[1], h[2], h[3]);
+          fixed |= fix;
+        }
+        for (int i = valid * 8 + lane; i < kBN * 8; i += 32) v[i] = make_uint4(0, 0, 0, 0);
+      }
+      if (fixed) *bad_v = 1;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&v_fixed[c - c_tree]));
     }
-  } else if (warp == 1) {
-    // ----------------------------------- MMA -----------------------------------
-    if (lane == 0 && nch > 0) {
-      constexpr uint32_t idesc_s = umma_idesc_bf16(kBM, kBN, 0, 0);
+    for (int c = (n > vst ? n - vst : 0); c < n; ++c)
+      if (c != withhold) ok = wait_phase(smem_u32(&v_full[c % vst]), (c / vst) & 1) && ok;
+    if (!ok && lane == 0) set_status(MD_DEV_TIMEOUT);
+  } else {
+    // --------------------------- MMAs: warp 1 + 2 w, stream w ---------------------------
+    // The whole warp walks the stream's jobs, convergent; one elected lane issues.
+    // A warp per stream: one stream's waits do not keep the other's MMAs back.
+    if (nch > 0) {
+      constexpr uint32_t idesc_s = umma_idesc_bf16(kBM, kSub, 0, 0);
       constexpr uint32_t idesc_o = umma_idesc_bf16(kBM, DH, 0, 1);
-      bool ok = mbar_wait(smem_u32(q_full), 0);
-      // S_w = Q K_c^T; the last stream to use the chunk frees its slot
-      auto issue_s = [&](int c, int w) -> bool {
-        const int st = c % kKStages;
-        if (!mbar_wait(smem_u32(&k_full[st]), (c / kKStages) & 1)) return false;
-        tc_fence_after();
-        const uint32_t sq = smem_u32(sQ + (two ? w : 0) * C::kTile), sk = smem_u32(sK + st * C::kTile);
+      const int w = warp >> 1;
+      const uint32_t tS = __reduce_max_sync(0xffffffffu, tmem) + w * 128, tO = tS + 256;
+      const int n = __reduce_max_sync(0xffffffffu, nsub), ct = __reduce_max_sync(0xffffffffu, c_tree);
+      const uint32_t q_desc = smem_u32(sQ), k_desc = smem_u32(sK), v_desc = smem_u32(sV);
+      if (w == 1 && lane == 0) {                         // the Q tiles
+        const uint32_t qb = smem_u32(q_full);
+        const int tiles = two ? 2 : 1;
+        mbar_arrive_expect_tx(qb, uint32_t(tiles * a.tpt * a.G) * DH * 2);
+        for (int i = 0; i < tiles; ++i)
 #pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb) {
-          const uint64_t ad = umma_desc_sw128(sq + kb * (kBM * 128), 16, 1024);
-          const uint64_t bd = umma_desc_sw128(sk + kb * (kBN * 128), 16, 1024);
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_3d(smem_u32(sQ + i * C::kQTile + kb * (kBM * 128)), &qmap, kb * 64, hk * a.G,
+                        b * T + tok0 + i * a.tpt, qb);
+      }
+      __syncwarp();
+      bool ok = __all_sync(0xffffffffu, wait_phase(smem_u32(q_full), 0));
+      // TILES row tiles: a job is half a chunk, the next job the next half (2), or the
+      // same half of the next chunk, the other stream having taken the other (1)
+      auto walk = [&](auto tiles_tag) {
+        constexpr int TILES = decltype(tiles_tag)::value;
+        constexpr int VST = TILES == 2 ? 2 : 3;
+        const int jobs = TILES == 2 ? n : (n - w + 1) / 2;
+        int ks = 0, kph = 0, vs = 0, vph = 0;            // slot and phase of the next job's K and V
+        auto half_of = [&](int j) { return TILES == 2 ? j & 1 : w; };
+        auto issue_s = [&](int j, int buf) {
+          const int half = half_of(j);
+          if (TILES == 1 || half == 0) {                 // a chunk this stream has not used yet
+            ok = __all_sync(0xffffffffu, wait_phase(smem_u32(&k_full[ks]), kph));
+            tc_fence_after();
+          }
+          if (!ok) return;
+          const uint64_t ad = umma_desc_sw128(q_desc + (TILES == 2 ? w : 0) * C::kQTile, 16, 1024);
+          const uint64_t bd = umma_desc_sw128(k_desc + ks * C::kTile + half * (kSub * 128), 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f16(tmem + w * 128, ad + uint64_t((kk * 32) >> 4), bd + uint64_t((kk * 32) >> 4), idesc_s, (kb | kk) != 0);
-        }
-        umma_commit(smem_u32(&s_full[w]));
-        if (!two || w == 1) umma_commit(smem_u32(&k_empty[st]));
-        return true;
+          for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_elect(tS + buf * kSub, ad + uint64_t((kb * (kBM * 128) + kk * 32) >> 4),
+                             bd + uint64_t((kb * (kBN * 128) + kk * 32) >> 4), idesc_s, (kb | kk) != 0);
+          umma_commit_elect(smem_u32(&s_full[2 * w + buf]));
+          if (TILES == 1 || half == 1 || j == jobs - 1) {
+            umma_commit_elect(smem_u32(&k_empty[ks]));
+            if (++ks == kKStages) { ks = 0; kph ^= 1; }
+          }
+        };
+        // O += P V of job j, then the S that follows in its buffer
+        auto job = [&](int j, int buf, int ph) {
+          const int half = half_of(j);
+          if (TILES == 1 || half == 0) {                 // a chunk this stream has not used yet
+            const int c = TILES == 1 ? j : j >> 1;
+            ok = c < ct ? wait_phase(smem_u32(&v_full[vs]), vph) : wait_phase(smem_u32(&v_fixed[c - ct]), 0);
+          }
+          ok = __all_sync(0xffffffffu, ok && wait_phase(smem_u32(&p_full[2 * w + buf]), ph));
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t vb = (VST == 3 && vs == 2 ? q_desc + C::kQTile : v_desc + vs * C::kTile) + half * (kSub * 128);
+          const uint64_t bd = umma_desc_sw128(vb, kBN * 128, 1024);
+#pragma unroll
+          for (int part = 0; part < C::kParts; ++part)
+#pragma unroll
+            for (int kk = 0; kk < kSub / 16; ++kk)
+              umma_f16_tmem_a_elect(tO, tS + buf * kSub + uint32_t(part * (kSub / 2) + kk * 8), bd + uint64_t((kk * 2048) >> 4),
+                                    idesc_o, (part | kk) != 0 ? 1u : uint32_t(j > 0));
+          umma_commit_elect(smem_u32(&o_full[w]));
+          if (TILES == 1 || half == 1 || j == jobs - 1) {
+            umma_commit_elect(smem_u32(&v_empty[vs]));
+            if (++vs == VST) { vs = 0; vph ^= 1; }
+          }
+          if (j + C::kBufs < jobs) issue_s(j + C::kBufs, buf);
+        };
+#pragma unroll
+        for (int j = 0; j < C::kBufs; ++j)
+          if (j < jobs && ok) issue_s(j, j);
+        int ph = 0;
+        for (int j0 = 0; j0 < jobs && ok; j0 += C::kBufs, ph ^= 1)
+#pragma unroll
+          for (int i = 0; i < C::kBufs; ++i)
+            if (j0 + i < jobs && ok) job(j0 + i, i, ph);
       };
-      const int step = two ? 1 : 2;                      // a stream's next chunk
-      if (ok) ok = issue_s(0, 0);
-      if (ok && two) ok = issue_s(0, 1);
-      if (ok && !two && nch > 1) ok = issue_s(1, 1);
-      const int jobs = two ? 2 * nch : nch;
-      for (int j = 0; j < jobs && ok; ++j) {
-        const int w = j & 1, c = two ? j >> 1 : j, nth = j >> 1;     // nth chunk of this stream
-        const int st = c % vst;
-        if (!mbar_wait(smem_u32(&p_full[w]), nth & 1) || !mbar_wait(smem_u32(&v_full[st]), (c / vst) & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t bd = umma_desc_sw128(smem_u32(v_slot(st)), kBN * 128, 1024);
-#pragma unroll
-        for (int part = 0; part < (F32 ? 2 : 1); ++part)
-#pragma unroll
-          for (int kk = 0; kk < kBN / 16; ++kk)
-            umma_f16_tmem_a(tmem + 256 + w * 128, tmem + w * 128 + uint32_t((kk >> 1) * 32 + part * 16 + (kk & 1) * 8),
-                            bd + uint64_t((kk * 2048) >> 4), idesc_o, (nth | part | kk) != 0);
-        if (!two || w == 1) umma_commit(smem_u32(&v_empty[st]));
-        if (c + step < nch) ok = issue_s(c + step, w);
+      if (ok) {
+        if (two) walk(IntTag<2>{});
+        else walk(IntTag<1>{});
       }
       // every MMA issued so far completes before TMEM is read out or released
-      umma_commit(smem_u32(mma_done));
-      if (!mbar_wait(smem_u32(mma_done), 0)) ok = false;
-      if (!ok) set_status(MD_DEV_TIMEOUT);
+      umma_commit_elect(smem_u32(mma_done));
+      if (!wait_phase(smem_u32(mma_done), 0)) ok = false;
+      if (!ok && lane == 0) set_status(MD_DEV_TIMEOUT);
     }
+    }
+    __syncwarp();
+    cluster_sync();                      // the softmax warps' two barriers
+    cluster_sync();
   } else {
     // --------------------------------- softmax ---------------------------------
-    const int w = (warp - 4) >> 2;                       // stream
+    const int w = (warp - 4) >> 3;                       // stream
+    const int half = ((warp - 4) >> 2) & 1;              // of a job's keys, and of O's columns
     const int q = warp & 3;                              // TMEM lane quarter
+    const int pair_bar = 1 + w * 4 + q;                  // named barrier of the two halves' warps
     const int r = q * 32 + lane;                         // row of the tile
     const int tile_tok = tok0 + (two ? w * a.tpt : 0);
     const int t = tile_tok + r / a.G;
@@ -343,137 +522,117 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t anc_lo = (uint64_t(tp.anc[tt][1]) << 32) | tp.anc[tt][0];
     const uint64_t anc_hi = (uint64_t(tp.anc[tt][3]) << 32) | tp.anc[tt][2];
     const float sc = a.scale_log2;
-    const int my_jobs = two ? nch : (nch - w + 1) / 2;
+    const int my_jobs = two ? nsub : (nsub - w + 1) / 2;
     float run_m = -INFINITY, run_l = 0.f;
     bool ok = true;
     for (int j = 0; j < my_jobs; ++j) {
-      const int c = two ? j : 2 * j + w;
-      if (ok && !mbar_wait(smem_u32(&s_full[w]), j & 1)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      const int u = two ? j : 2 * j + w;                 // half-chunk
+      const int buf = j % C::kBufs;
+      // A wait that gives up only skips work: every iteration runs the halves' barriers.
+      ok = __all_sync(0xffffffffu, ok && wait_phase(smem_u32(&s_full[2 * w + buf]), (j / C::kBufs) & 1));
       tc_fence_after();
-      const int key0 = (c_begin + c) * kBN;
+      const uint32_t tSb = tS + buf * kSub;
+      const int key0 = c_begin * kBN + u * kSub;
       if (warp_live) {
-        // two readings of S, 64 and 32 columns at a time: the whole row in registers spills
-        const bool masked = key0 + kBN > P;              // tree slots, or slots behind them
-        float s[64];
-        float m8[8];
+        float s[32];
+        if (ok) tmem_ld32_async(tSb + half * 32, s);
+        tmem_ld_wait();
+        settle(s);
+        const bool masked = key0 + kSub > P;             // tree slots, or slots behind them
+        if (masked) {
+          const uint32_t vis = uint32_t(visible_bits(anc_lo, anc_hi, key0 + half * 32 - P));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m8[i] = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          tmem_ld32_async(tS + 64 * g, s);
-          tmem_ld32_async(tS + 64 * g + 32, s + 32);
-          tmem_ld_wait();
-          settle(s);
-          settle(s + 32);
-          if (masked) {
-            const uint64_t vis = visible_bits(anc_lo, anc_hi, key0 + 64 * g - P);
-#pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = ((vis >> i) & 1ull) ? s[i] : -INFINITY;
-          }
-#pragma unroll
-          for (int i = 0; i < 64; ++i) m8[i & 7] = fmaxf(m8[i & 7], s[i]);
+          for (int i = 0; i < 32; ++i) s[i] = ((vis >> i) & 1u) ? s[i] : -INFINITY;
         }
-        tmem_ld32_async(tS, s);                          // the first columns of the second reading
-        float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+        float m4[4];                                     // four chains of three-way maxima
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          m4[k] = max3(s[k], s[k + 4], s[k + 8]);
+          m4[k] = max3(m4[k], s[k + 12], s[k + 16]);
+          m4[k] = max3(m4[k], s[k + 20], s[k + 24]);
+          m4[k] = max3(m4[k], s[k + 28], s[k + 28]);
+        }
+        float mx = max3(max3(m4[0], m4[1], m4[2]), m4[3], m4[3]);
+        // the row's maximum over both halves; behind the second barrier both have
+        // read their scores, and either may write P over them
+        named_bar_sync(pair_bar, 64);                    // the last job's maxima have been read
+        s_part[(2 * w + half) * kBM + r] = mx;
+        named_bar_sync(pair_bar, 64);
+        const float mo = s_part[(2 * w + (half ^ 1)) * kBM + r];
+        mx = max3(mx, mo, mo);
+        // a score that is NaN or infinite makes the row NaN, as its softmax is
+        if (!(mx < INFINITY)) run_l = __int_as_float(0x7FC00000);
         mx = (mx == -INFINITY) ? -INFINITY : mx * sc;
         const bool up = mx > run_m + kRescaleLog2 || (run_m == -INFINITY && mx != -INFINITY);
-        const float m_new = up ? mx : run_m;
-        const float fold = (up && run_m != -INFINITY) ? exp2f(run_m - m_new) : 1.f;
-        if (__any_sync(0xffffffffu, fold != 1.f)) {
+        if (__any_sync(0xffffffffu, up)) {
+          const float fold = (up && run_m != -INFINITY) ? exp2f(run_m - mx) : 1.f;
+          if (__any_sync(0xffffffffu, fold != 1.f)) {
+            // O is rescaled in place, half of its columns here: this stream's last P V has
+            // landed (the one before it has, as S of this job was issued behind it)
+            if (ok) ok = __all_sync(0xffffffffu, wait_phase(smem_u32(&o_full[w]), (j - 1) & 1));
+            tc_fence_after();
+#pragma unroll 1
+            for (int e0 = half * (DH / 2); e0 < (half + 1) * (DH / 2); e0 += 16) {
+              float o[16];
+              tmem_ld16(tO + e0, o);
 #pragma unroll
-          for (int e0 = 0; e0 < DH; e0 += 32) {
-            float o[32];
-            tmem_ld32(tO + e0, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= fold;
-            tmem_st32(tO + e0, o);
-          }
-        }
-        run_l *= fold;
-        run_m = m_new;
-        const float mb = (run_m == -INFINITY) ? 0.f : run_m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int g = 0; g < kBN / 32; ++g) {
-          float* x = s + 32 * (g & 1);
-          tmem_ld_wait();
-          settle(x);
-          if (g < 3) tmem_ld32_async(tS + 32 * (g + 1), s + 32 * ((g + 1) & 1));
-          if (masked) {
-            const uint32_t vis = uint32_t(visible_bits(anc_lo, anc_hi, key0 + 32 * g - P));
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = ((vis >> i) & 1u) ? x[i] : -INFINITY;
-          }
-          uint32_t ph[16], pl[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float p0 = exp2_sfu(fmaf(x[i], sc, -mb));
-            const float p1 = exp2_sfu(fmaf(x[i + 1], sc, -mb));
-            sum[(i >> 1) & 3] += p0 + p1;
-            if constexpr (F32) {
-              const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-              ph[i >> 1] = __byte_perm(u0, u1, 0x7632);              // truncated to bf16
-              const float r0 = p0 - __uint_as_float(u0 & 0xFFFF0000u);
-              const float r1 = p1 - __uint_as_float(u1 & 0xFFFF0000u);
-              pl[i >> 1] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
-            } else {
-              ph[i >> 1] = pack_bf16x2(p0, p1);
+              for (int e = 0; e < 16; ++e) o[e] *= fold;
+              tmem_st16(tO + e0, o);
             }
           }
-          tmem_st16u(tS + 32 * g, ph);                   // over the 32 scores just read
-          if constexpr (F32) tmem_st16u(tS + 32 * g + 16, pl);
+          run_l *= fold;
+          run_m = up ? mx : run_m;
+        }
+        const float mb = (run_m == -INFINITY) ? 0.f : run_m;
+        const f32x2 sc2 = pair(sc, sc), mb2 = pair(-mb, -mb);
+        f32x2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        uint32_t p0[16];
+        [[maybe_unused]] uint32_t p1[16], p2[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float a0, a1;
+          unpair(fma2(pair(s[2 * i], s[2 * i + 1]), sc2, mb2), a0, a1);
+          a0 = exp2_sfu(a0);
+          a1 = exp2_sfu(a1);
+          sum[i & 1] = add2(sum[i & 1], pair(a0, a1));
+          if constexpr (F32) {
+            // truncated parts, 8 bits each: the remainders are exact
+            p0[i] = high_halves(a0, a1);
+            const float b0 = a0 - high_part(a0), b1 = a1 - high_part(a1);
+            p1[i] = high_halves(b0, b1);
+            p2[i] = pack_bf16x2(b0 - high_part(b0), b1 - high_part(b1));
+          } else {
+            p0[i] = pack_bf16x2(a0, a1);
+          }
+        }
+        tmem_st16u(tSb + half * 16, p0);
+        if constexpr (F32) {
+          tmem_st16u(tSb + kSub / 2 + half * 16, p1);
+          tmem_st16u(tSb + kSub + half * 16, p2);
         }
         tmem_st_wait();
-        run_l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      }
-      // V rows that P's zeros must not meet
-      if (key0 + kBN > P && (!two || w == 0)) {
-        const int st = c % vst;
-        if (!mbar_wait(smem_u32(&v_full[st]), (c / vst) & 1)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        uint8_t* v = v_slot(st);
-        const int valid = min(kBN, nkeys - key0);
-        const int tree0 = max(0, P - key0);              // first row of a tree node
-        for (int i = r; i < kBN * C::KB * 8; i += kBM) { // 16-byte pieces, kb-major
-          const int row = (i >> 3) & (kBN - 1);
-          uint4* piece = reinterpret_cast<uint4*>(v) + i;
-          if (row >= valid) {
-            *piece = make_uint4(0, 0, 0, 0);
-          } else if (row >= tree0 && T > 1) {
-            uint4 x = *piece;
-            uint32_t u[4] = {x.x, x.y, x.z, x.w};
-            bool fix = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (!bf16_finite(u[e])) { u[e] &= 0xFFFF0000u; fix = true; }
-              if (!bf16_finite(u[e] >> 16)) { u[e] &= 0x0000FFFFu; fix = true; }
-            }
-            if (fix) {
-              *piece = make_uint4(u[0], u[1], u[2], u[3]);
-              *bad_v = 1;
-            }
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        float l0, l1;
+        unpair(add2(sum[0], sum[1]), l0, l1);
+        run_l += l0 + l1;
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
+      if (lane == 0 && ok) mbar_arrive(smem_u32(&p_full[2 * w + buf]));
     }
     if (!ok) set_status(MD_DEV_TIMEOUT);
     // the stream's O and (m, sum), staged over the idle tiles and ring: every MMA
     // of the CTA is done, so nothing reads or fills them any more
     bool staged = ok && my_jobs > 0;
-    if (nch > 0) staged = __all_sync(0xffffffffu, mbar_wait(smem_u32(mma_done), 0)) && staged;
-    named_bar_sync(1, kSoftThreads);                     // both streams are past their last look at the ring
+    if (nch > 0) staged = __all_sync(0xffffffffu, wait_phase(smem_u32(mma_done), 0)) && staged;
+    if (c_tree < nch) staged = __all_sync(0xffffffffu, wait_phase(smem_u32(&v_fixed[nch - 1 - c_tree]), 0)) && staged;   // *bad_v
+    if (warp_live) named_bar_sync(pair_bar, 64);         // the last maxima have been read
+    if (half == 1) s_part[(2 * w + 1) * kBM + r] = run_l;
+    named_bar_sync(9, kSoftThreads);                     // both streams are past their last look at the ring
     float* sO = reinterpret_cast<float*>(smem) + size_t(w) * kBM * C::kLd;
     if (staged && warp_live) {
       tc_fence_after();
 #pragma unroll
-      for (int e0 = 0; e0 < DH; e0 += 32) {
+      for (int e0 = half * (DH / 2); e0 < (half + 1) * (DH / 2); e0 += 32) {
         float o[32];
         tmem_ld32(tO + e0, o);
 #pragma unroll
@@ -484,23 +643,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // elements of visible nodes' V that are not finite, left out of P V
         for (int n = 0; n < T; ++n) {
           if (!((tp.anc[t][n >> 5] >> (n & 31)) & 1u)) continue;
-          const int slot = P + n, c = slot / kBN - c_begin;
-          if (c < 0 || c >= nch || (!two && (c & 1) != w)) continue;
+          const int slot = P + n, u = (slot - c_begin * kBN) / kSub;
+          if (slot < c_begin * kBN || u >= nsub || (!two && (u & 1) != w)) continue;
           const int pg = trow[slot / a.page];
           if (pg < 0 || pg >= a.pool) continue;
           const uint16_t* v = a.v_pages + ((size_t(pg) * a.Hkv + hk) * a.page + slot % a.page) * DH;
-          for (int e = 0; e < DH; ++e)
+          for (int e = half * (DH / 2); e < (half + 1) * (DH / 2); ++e)
             if (!bf16_finite(v[e])) sO[r * C::kLd + e] += bf16_to_f32(v[e]);
         }
       }
     }
-    sML[w * kBM + r] = make_float2(staged ? run_m : -INFINITY, staged ? run_l : 0.f);
-  }
+    if (half == 0)
+      sML[w * kBM + r] = staged ? make_float2(run_m, run_l + s_part[(2 * w + 1) * kBM + r]) : make_float2(-INFINITY, 0.f);
 
-  // ------------------- join the streams and splits of each row -------------------
-  __syncwarp();
-  cluster_sync();                        // every split's streams are staged
-  if (warp >= 4) {
+    // ----------------- join the streams and splits of each row -----------------
+    __syncwarp();
+    cluster_sync();                      // every split's streams are staged
     // a row's partial results: (split, stream) with one tile, (split) with two
     const int np = two ? a.splits : 2 * a.splits;
     const int ntok = min(two ? 2 * a.tpt : a.tpt, T - tok0);
@@ -508,57 +666,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile_rows = a.tpt * a.G;
     const int crank = int(cluster_ctarank());
     const int r0 = rows * crank / a.splits, r1 = rows * (crank + 1) / a.splits;
-    constexpr int kLanes = DH / 4;                       // float4 columns: 32 or 16 lanes a row
-    constexpr int kRowsPerWarp = 32 / kLanes;
-    const int sub = lane / kLanes, col = lane % kLanes;
-    for (int i0 = r0 + (warp - 4) * kRowsPerWarp; i0 < r1; i0 += 8 * kRowsPerWarp) {
-      const int i = min(i0 + sub, r1 - 1);               // the last pair may repeat a row
-      const int w0 = i / tile_rows, row = i - w0 * tile_rows;          // stream (two tiles) and row in it
-      // lane p holds partial p of this warp's row (two rows a warp: 16 lanes each)
-      float m_p = -INFINITY, l_p = 0.f, m2 = -INFINITY, l2 = 0.f;
-      auto ml_of = [&](int p) -> float2 {
-        const int sp = two ? p : p >> 1, st = two ? w0 : p & 1;
-        return ld_cluster_f2(mapa_shared(smem_u32(&sML[st * kBM + row]), uint32_t(sp)));
-      };
-      if (col < np) { const float2 x = ml_of(col); m_p = x.x; l_p = x.y; }
-      if (kLanes == 16 && col + 16 < np) { const float2 x = ml_of(col + 16); m2 = x.x; l2 = x.y; }
-      float mx = fmaxf(m_p, m2);
-#pragma unroll
-      for (int d = kLanes / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      const float w_p = (m_p == -INFINITY) ? 0.f : exp2f(m_p - mx), w_2 = (m2 == -INFINITY) ? 0.f : exp2f(m2 - mx);
-      float L = l_p * w_p + l2 * w_2;
-#pragma unroll
-      for (int d = kLanes / 2; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+    const int tid = threadIdx.x - (kThreads - kSoftThreads);
+    // This code runs once a CTA, so what it costs is fetching it: loops stay rolled.
+    // Weights of the partial results first: sW[row][p] = 2^(m_p - m) / L, or -1 where
+    // nothing was staged; from (m, sum) of every partial, copied to sP[row][p].
+    float2* sP = sML + 2 * kBM;
+    float* sW = reinterpret_cast<float*>(sP + 2 * kBM + 2 * kMaxSplits);
+    const int nw = (r1 - r0) * np;
+    if (tid < nw) {                                      // at most 2 * 128 + 2 * 16 pairs
+      const int i = tid / np, p = tid - i * np;
+      const int w0 = (r0 + i) / tile_rows, row = r0 + i - w0 * tile_rows;   // stream (two tiles) and row in it
+      sP[tid] = ld_cluster_f2(mapa_shared(smem_u32(&sML[(two ? w0 : p & 1) * kBM + row]), uint32_t(two ? p : p >> 1)));
+    }
+    named_bar_sync(9, kSoftThreads);
+    if (tid < nw) {
+      const int i = tid / np;
+      float mx = -INFINITY, L = 0.f;
+#pragma unroll 2
+      for (int p = 0; p < np; ++p) mx = fmaxf(mx, sP[i * np + p].x);
+#pragma unroll 2
       for (int p = 0; p < np; ++p) {
-        const int from = sub * kLanes + (p & (kLanes - 1));
-        const float wgt = __shfl_sync(0xffffffffu, (kLanes == 16 && p >= 16) ? w_2 : w_p, from);
-        const float mm = __shfl_sync(0xffffffffu, (kLanes == 16 && p >= 16) ? m2 : m_p, from);
-        if (mm != -INFINITY) {                           // a stream without chunks staged nothing
-          const int sp = two ? p : p >> 1, st = two ? w0 : p & 1;
-          const float* src = reinterpret_cast<float*>(smem) + (size_t(st) * kBM + row) * C::kLd + col * 4;
-          const float4 o = ld_cluster_f4(mapa_shared(smem_u32(src), uint32_t(sp)));
-          acc.x = fmaf(o.x, wgt, acc.x);
-          acc.y = fmaf(o.y, wgt, acc.y);
-          acc.z = fmaf(o.z, wgt, acc.z);
-          acc.w = fmaf(o.w, wgt, acc.w);
+        const float2 ml = sP[i * np + p];
+        L += ml.x == -INFINITY ? 0.f : ml.y * exp2_sfu(ml.x - mx);
+      }
+      const float m = sP[tid].x;
+      sW[tid] = m == -INFINITY ? -1.f : exp2_sfu(m - mx) / L;
+    }
+    named_bar_sync(9, kSoftThreads);
+    // rows as float4 columns, up to kP of a thread's loads from the cluster in flight
+    constexpr int kF4 = DH / 4, kP = 8;
+    const int items = (r1 - r0) * kF4;
+#pragma unroll 1
+    for (int i = tid; i < items; i += kSoftThreads) {
+      const int pr = r0 + i / kF4;                       // (node, head) pair of the unit
+      const int w0 = pr / tile_rows, row = pr - w0 * tile_rows;
+      const float* sw = sW + (i / kF4) * np;
+      const uint32_t src = smem_u32(smem) + uint32_t((row * C::kLd + (i % kF4) * 4) * 4);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int p0 = 0; p0 < np; p0 += kP) {
+        float4 o[kP];
+        float wgt[kP];
+#pragma unroll
+        for (int e = 0; e < kP; ++e) {
+          const int p = p0 + e;
+          wgt[e] = p < np ? sw[p] : -1.f;
+          const int st = two ? w0 : p & 1, sp = two ? p : p >> 1;
+          o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (!(wgt[e] < 0.f)) o[e] = ld_cluster_f4(mapa_shared(src + st * (kBM * C::kLd * 4), uint32_t(sp)));
+        }
+#pragma unroll
+        for (int e = 0; e < kP; ++e) {
+          const float x = wgt[e] < 0.f ? 0.f : wgt[e];
+          acc.x = fmaf(o[e].x, x, acc.x);
+          acc.y = fmaf(o[e].y, x, acc.y);
+          acc.z = fmaf(o[e].z, x, acc.z);
+          acc.w = fmaf(o[e].w, x, acc.w);
         }
       }
-      const float inv = 1.f / L;
-      float4 y = bad ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-      if (i0 + sub < r1) {
-        const int tn = tok0 + i / a.G, h = hk * a.G + i % a.G;
-        const size_t at = ((size_t(b) * T + tn) * a.Hq + h) * DH + col * 4;
-        if constexpr (F32)
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
-        else
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-      }
+      if (bad) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const size_t at = ((size_t(b) * T + tok0 + pr / a.G) * a.Hq + hk * a.G + pr % a.G) * DH + (i % kF4) * 4;
+      if constexpr (F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = acc;
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
     }
+    __syncwarp();
+    cluster_sync();                      // peers are done reading this CTA's shared memory
   }
-  __syncwarp();
-  cluster_sync();                        // peers are done reading this CTA's shared memory
+
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

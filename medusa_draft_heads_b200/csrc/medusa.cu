@@ -880,7 +880,7 @@ void paged_attn_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, dim3 
   *cfg = {};
   cfg->gridDim = grid;
   cfg->blockDim = dim3(md::attn_paged::kThreads);
-  cfg->dynamicSmemBytes = md::attn_paged::Cfg<DH>::kSmem;
+  cfg->dynamicSmemBytes = md::attn_paged::Cfg<DH, F32>::kSmem;
   cfg->stream = st;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = grid.x;
@@ -892,12 +892,20 @@ void paged_attn_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, dim3 
   cfg->numAttrs = 2;
 }
 
+// Function attributes last for the process: set once per device (a call of
+// cudaFuncSetAttribute costs about a microsecond).
 template <int DH, bool F32>
 md_status paged_attn_attributes() {
-  auto kern = md::attn_paged::attn_paged_kernel<DH, F32>;
-  md_status s = set_smem(kern, md::attn_paged::Cfg<DH>::kSmem);
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  md_status s = cuda_ok(cudaGetDevice(&dev));
   if (s != MD_OK) return s;
-  return cuda_ok(cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return MD_OK;
+  auto kern = md::attn_paged::attn_paged_kernel<DH, F32>;
+  if ((s = set_smem(kern, md::attn_paged::Cfg<DH, F32>::kSmem)) != MD_OK) return s;
+  if ((s = cuda_ok(cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1))) != MD_OK) return s;
+  if (dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+  return MD_OK;
 }
 
 // CTAs resident at once in clusters of `splits` on the current device.
@@ -925,33 +933,50 @@ int paged_attn_slots(int splits) {
 }
 
 struct PagedAttnPlan {
-  int tpt, units, splits, sort;
+  int tpt, tpu, units, splits, sort;
 };
 
-// Row tiles hold whole nodes (G rows each); a unit is up to two tiles. The KV
-// splits are those that a count of waves finds shortest: every wave costs its
-// share of the chunks the table can hold, plus about three chunks' time for
-// the CTA's set-up, first loads and join (3 to 4 us against 1.1 us a chunk).
+// Row tiles hold whole nodes (G rows each); a unit is one or two tiles, and its
+// KV range is cut into splits. The shape with the least estimated time (us) is
+// taken, from measured costs: a CTA's fixed part (launch, first loads, read-out)
+// 8 and 10 for one and two tiles, 1.5 more to join splits; a chunk 0.8 for one
+// tile, 1.1 if other tiles' CTAs read the same keys from L2, 1.75 for two; CTAs
+// past one wave fill the SMs as they come, with half a CTA's time left uneven; and
+// no call is faster than its keys' bytes from memory. Chunks are counted by
+// what the table can hold: the lengths are on the device.
+//   70B tree, B = 1 (40 tiles, 33 chunks): one tile, 3 splits 23.7 us; two tiles, 5
+//     splits 26.7. B = 8: one tile 124, two tiles 113.6.
+//   Decoding, 8 KV heads, 4096 slots: 1 split 32.9, 4 15.3, 8 12.5, 12 (two waves)
+//     22.6. 16 requests of 26000: 1 split 261, 2 276.
 PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, int max_pages, bool f32) {
   PagedAttnPlan p;
   const int G = Hq / Hkv;
   p.tpt = md::attn_paged::kBM / G;
-  p.units = (T + 2 * p.tpt - 1) / (2 * p.tpt);
-  const int64_t base = int64_t(B) * Hkv * p.units;
+  const int tiles = (T + p.tpt - 1) / p.tpt;
   const int chunks = int((int64_t(max_pages) * page + md::attn_paged::kBN - 1) / md::attn_paged::kBN);
+  const double bytes_us = 4.0 * B * Hkv * dh * md::attn_paged::kBN * chunks / 6.5e6;
   double best = 0;
-  p.splits = 1;
-  p.sort = 0;
-  for (int s = 1; s <= md::attn_paged::kMaxSplits && s <= chunks; ++s) {
-    const int slots = dh == 128 ? (f32 ? paged_attn_slots<128, true>(s) : paged_attn_slots<128, false>(s))
-                                : (f32 ? paged_attn_slots<64, true>(s) : paged_attn_slots<64, false>(s));
-    if (slots < s) continue;
-    const int64_t waves = (base * s + slots - 1) / slots;
-    const double cost = double(waves) * (double((chunks + s - 1) / s) + 3.0);
-    if (best == 0 || cost < best) {
-      best = cost;
-      p.splits = s;
-      p.sort = B > 1 && waves > 1;
+  for (int tpu = 1; tpu <= 2 && tpu <= tiles; ++tpu) {
+    const int units = (tiles + tpu - 1) / tpu;
+    const int64_t base = int64_t(B) * Hkv * units;
+    for (int s = 1; s <= md::attn_paged::kMaxSplits && s <= chunks; ++s) {
+      const int slots = dh == 128 ? (f32 ? paged_attn_slots<128, true>(s) : paged_attn_slots<128, false>(s))
+                                  : (f32 ? paged_attn_slots<64, true>(s) : paged_attn_slots<64, false>(s));
+      if (slots < s) continue;
+      const int per_cta = (chunks + s - 1) / s;
+      const double join = s > 1 ? 1.5 : 0.0;
+      const double one = per_cta * (tiles > 1 ? 1.1 : 0.8) + 8.0 + join, two = per_cta * 1.75 + 10.0 + join;
+      const double longest = tpu == 2 ? two : one;
+      const double all = tpu == 2 ? (tiles / 2) * two + (tiles % 2) * one : tiles * one;   // a KV head's units, one split
+      const bool waves = base * s > slots;
+      const double us = std::max(waves ? double(B) * Hkv * s * all / slots + 0.5 * longest : longest, bytes_us + 8.0);
+      if (best == 0 || us < best) {
+        best = us;
+        p.tpu = tpu;
+        p.units = units;
+        p.splits = s;
+        p.sort = B > 1 && waves;
+      }
     }
   }
   return p;
@@ -1602,7 +1627,7 @@ md_status md_tree_attention_paged(const md_bf16* q, const md_bf16* k_pages, cons
   a.v_pages = v_pages; a.table = block_table; a.prefix_len = prefix_len; a.out = out;
   a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.pool = pool_pages; a.page = page_size; a.max_pages = max_pages;
   a.piece = std::min(page_size & -page_size, md::attn_paged::kBN);
-  a.tpt = pl.tpt; a.units = pl.units; a.splits = pl.splits; a.sort = pl.sort;
+  a.tpt = pl.tpt; a.tpu = pl.tpu; a.units = pl.units; a.splits = pl.splits; a.sort = pl.sort;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(float(dh))) * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (out_type == MD_OUT_F32)
