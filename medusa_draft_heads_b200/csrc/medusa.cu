@@ -908,12 +908,10 @@ md_status paged_attn_attributes() {
   return MD_OK;
 }
 
-// CTAs resident at once in clusters of `splits` on the current device.
+// CTAs resident at once in clusters of `splits` on the current device, dev.
 template <int DH, bool F32>
-int paged_attn_slots(int splits) {
+int paged_attn_slots(int dev, int splits) {
   static std::atomic<int> cache[kMaxDevices][md::attn_paged::kMaxSplits + 1];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   int n = cache[dev][splits].load(std::memory_order_relaxed);
   if (n == 0) {                          // stored as count + 1
     int clusters = 0;
@@ -939,8 +937,9 @@ struct PagedAttnPlan {
 // Row tiles hold whole nodes (G rows each); a unit is one or two tiles, and its
 // KV range is cut into splits. The shape with the least estimated time (us) is
 // taken, from measured costs: a CTA's fixed part (launch, first loads, read-out)
-// 8 and 10 for one and two tiles, 1.5 more to join splits; a chunk 0.8 for one
-// tile, 1.1 if other tiles' CTAs read the same keys from L2, 1.75 for two; CTAs
+// 8 and 10 for one and two tiles, 0.5 and 1.5 more to join splits; a chunk 0.8 for
+// one tile, 1.1 if other tiles' CTAs read the same keys from L2, 1.75 for two, twice
+// that for fp32 results (one score buffer, three P V products); CTAs
 // past one wave fill the SMs as they come, with half a CTA's time left uneven; and
 // no call is faster than its keys' bytes from memory. Chunks are counted by
 // what the table can hold: the lengths are on the device.
@@ -952,7 +951,11 @@ PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, i
   PagedAttnPlan p;
   const int G = Hq / Hkv;
   p.tpt = md::attn_paged::kBM / G;
-  const int tiles = (T + p.tpt - 1) / p.tpt;
+  p.tpu = p.splits = 1;
+  p.sort = B > 1;
+  const int tiles = p.units = (T + p.tpt - 1) / p.tpt;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return p;
   const int chunks = int((int64_t(max_pages) * page + md::attn_paged::kBN - 1) / md::attn_paged::kBN);
   const double bytes_us = 4.0 * B * Hkv * dh * md::attn_paged::kBN * chunks / 6.5e6;
   double best = 0;
@@ -960,12 +963,13 @@ PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, i
     const int units = (tiles + tpu - 1) / tpu;
     const int64_t base = int64_t(B) * Hkv * units;
     for (int s = 1; s <= md::attn_paged::kMaxSplits && s <= chunks; ++s) {
-      const int slots = dh == 128 ? (f32 ? paged_attn_slots<128, true>(s) : paged_attn_slots<128, false>(s))
-                                  : (f32 ? paged_attn_slots<64, true>(s) : paged_attn_slots<64, false>(s));
+      const int slots = dh == 128 ? (f32 ? paged_attn_slots<128, true>(dev, s) : paged_attn_slots<128, false>(dev, s))
+                                  : (f32 ? paged_attn_slots<64, true>(dev, s) : paged_attn_slots<64, false>(dev, s));
       if (slots < s) continue;
       const int per_cta = (chunks + s - 1) / s;
-      const double join = s > 1 ? 1.5 : 0.0;
-      const double one = per_cta * (tiles > 1 ? 1.1 : 0.8) + 8.0 + join, two = per_cta * 1.75 + 10.0 + join;
+      const double slow = f32 ? 2.0 : 1.0;
+      const double one = per_cta * slow * (tiles > 1 ? 1.1 : 0.8) + 8.0 + (s > 1 ? 0.5 : 0.0);
+      const double two = per_cta * slow * 1.75 + 10.0 + (s > 1 ? 1.5 : 0.0);
       const double longest = tpu == 2 ? two : one;
       const double all = tpu == 2 ? (tiles / 2) * two + (tiles % 2) * one : tiles * one;   // a KV head's units, one split
       const bool waves = base * s > slots;
@@ -1664,10 +1668,24 @@ md_status md_qk_rope_append(const md_bf16* q, const md_bf16* k, const md_bf16* v
   a.k_pages = k_pages; a.v_pages = v_pages; a.table = block_table; a.prefix_len = prefix_len; a.n_new = n_new;
   a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.rot = rot; a.interleaved = interleaved != 0;
   a.max_pages = max_pages; a.pool = pool_pages; a.page = page_size; a.eps = eps;
-  const dim3 grid(B * T, 1);
+  // A CTA takes a run of tokens and a block of heads. Runs as long as about eight
+  // CTAs a SM are left: a tree's 65 tokens of 80 heads fill the SMs with runs of one (3.1
+  // us; a CTA per token 6.2); prompts use the angles and pointers of a CTA longest,
+  // and all the blocks of a token in turn (24k tokens of 48 heads: runs of 4 / 8 / 16
+  // 120 / 111 / 109 us; a CTA per block of heads 119).
+  const int64_t heads = int64_t(Hq) + 2 * Hkv, at_once = md::append::kThreads / (dh / 8);
+  const int blocks = int((heads + at_once - 1) / at_once);
+  a.block = int((heads + blocks - 1) / blocks);
+  const int64_t ctas = int64_t(num_sms()) * 8;
+  const bool all_heads = int64_t(B) * T >= ctas * md::append::kRun;
+  const int64_t fill = int64_t(B) * T * (all_heads ? 1 : blocks) / ctas;
+  a.run = int(std::max<int64_t>(1, std::min<int64_t>(fill, md::append::kRun)));
+  const dim3 grid(unsigned(int64_t(B) * ((T + a.run - 1) / a.run)), all_heads ? 1 : blocks);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dh == 128 ? launch_pdl(md::append::qk_rope_append_kernel<128>, grid, dim3(md::append::kThreads), 0, st, a)
-                   : launch_pdl(md::append::qk_rope_append_kernel<64>, grid, dim3(md::append::kThreads), 0, st, a);
+  const bool many = 2 * heads <= at_once;
+  auto kern = dh == 128 ? (many ? md::append::qk_rope_append_kernel<128, true> : md::append::qk_rope_append_kernel<128, false>)
+                        : (many ? md::append::qk_rope_append_kernel<64, true> : md::append::qk_rope_append_kernel<64, false>);
+  return launch_pdl(kern, grid, dim3(md::append::kThreads), 0, st, a);
 }
 
 md_status md_tree_commit_paged(md_bf16* k_pages, md_bf16* v_pages, int32_t layers, int32_t pool_pages,
@@ -1727,7 +1745,7 @@ md_status md_pages_fork(md_bf16* k_pages, md_bf16* v_pages, int32_t layers, int3
   if (s != MD_OK) return s;
   if (layers < 1) return MD_ERR_INVALID_ARG;
   if ((s = paged_check(B, pool_pages, page_size, max_pages, Hkv, dh)) != MD_OK) return s;
-  if (int64_t(layers) * Hkv > INT32_MAX) return MD_ERR_UNSUPPORTED;
+  if (int64_t(layers) * Hkv > INT32_MAX - md::pages::kCopyHeads) return MD_ERR_UNSUPPORTED;
   if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(refcount, 16)) return MD_ERR_INVALID_ARG;
   if (!ws || ws_bytes < need || !aligned(ws, 256)) return MD_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1736,9 +1754,10 @@ md_status md_pages_fork(md_bf16* k_pages, md_bf16* v_pages, int32_t layers, int3
   a.jobs = static_cast<md::pages::ForkJob*>(ws);
   a.B = B; a.n = n; a.max_pages = max_pages; a.pool = pool_pages; a.page = page_size;
   if ((s = launch_pdl(md::pages::pages_fork_kernel, dim3(1), dim3(md::pages::kThreads), 0, st, a)) != MD_OK) return s;
-  return launch_pdl(md::pages::pages_fork_copy_kernel, dim3(layers * Hkv, 2, n), dim3(256), 0, st,
+  const dim3 grid((layers * Hkv + md::pages::kCopyHeads - 1) / md::pages::kCopyHeads, 2, n);
+  return launch_pdl(md::pages::pages_fork_copy_kernel, grid, dim3(md::pages::kCopyThreads), 0, st,
                     reinterpret_cast<uint4*>(k_pages), reinterpret_cast<uint4*>(v_pages),
-                    static_cast<const md::pages::ForkJob*>(a.jobs), pool_pages, Hkv, page_size, dh / 8);
+                    static_cast<const md::pages::ForkJob*>(a.jobs), layers, pool_pages, Hkv, page_size, dh / 8);
 }
 
 md_status md_get_device_status(void* stream, int32_t* out, int32_t clear) {

@@ -16,7 +16,7 @@ namespace pages {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPerThread = 4;                    // counts per thread and scan tile
+constexpr int kPerThread = 16;                   // counts per thread and scan tile: four loads in flight
 constexpr int kTile = kThreads * kPerThread;
 constexpr int kMaxRows = 16384;                  // rows of a resize: their running needs sit in shared memory
 constexpr int kMaxForks = kThreads;              // forks of a call: one thread each
@@ -58,14 +58,18 @@ __device__ __forceinline__ void drop_page(int32_t* refcount, int pool, int page)
   }
 }
 
-// Bit i of the result: page (tile base + kPerThread * threadIdx.x + i) is free.
-// Counts are read past L1: the block's own atomics may just have changed them.
+// Bit i of the result: page base + kPerThread * threadIdx.x + i is free. Counts
+// are read past L1: the block's own atomics may just have changed them.
 __device__ __forceinline__ uint32_t free_bits(const int32_t* refcount, int pool, int base) {
   const int p0 = base + int(threadIdx.x) * kPerThread;
   uint32_t m = 0;
   if (p0 + kPerThread <= pool) {
-    const int4 c = __ldcg(reinterpret_cast<const int4*>(refcount + p0));
-    m = (c.x == 0 ? 1u : 0u) | (c.y == 0 ? 2u : 0u) | (c.z == 0 ? 4u : 0u) | (c.w == 0 ? 8u : 0u);
+    int4 c[kPerThread / 4];
+#pragma unroll
+    for (int i = 0; i < kPerThread / 4; ++i) c[i] = __ldcg(reinterpret_cast<const int4*>(refcount + p0) + i);
+#pragma unroll
+    for (int i = 0; i < kPerThread / 4; ++i)
+      m |= ((c[i].x == 0 ? 1u : 0u) | (c[i].y == 0 ? 2u : 0u) | (c[i].z == 0 ? 4u : 0u) | (c[i].w == 0 ? 8u : 0u)) << (4 * i);
   } else {
     for (int i = 0; i < kPerThread; ++i)
       if (p0 + i < pool && __ldcg(refcount + p0 + i) == 0) m |= 1u << i;
@@ -73,33 +77,21 @@ __device__ __forceinline__ uint32_t free_bits(const int32_t* refcount, int pool,
   return m;
 }
 
-// Free pages of the pool, counted by the whole block.
-__device__ __forceinline__ int count_free(const int32_t* refcount, int pool, int* part) {
-  int n = 0;
-  for (int base = 0; base < pool; base += kTile) n += __popc(free_bits(refcount, pool, base));
-  int total;
-  block_incl_scan(n, part, total);
-  return total;
-}
-
-// Calls take(rank, page) for the `want` lowest free pages (rank 0 .. want - 1).
+// Calls take(rank, page) for the `want` lowest free pages (rank 0 .. want - 1), or
+// for all of them if there are fewer; returns how many it found. The pool is
+// read once, up to the last page taken.
 template <typename Take>
-__device__ __forceinline__ void take_lowest_free(const int32_t* refcount, int pool, int want, int* part, Take take) {
+__device__ __forceinline__ int take_lowest_free(const int32_t* refcount, int pool, int want, int* part, Take take) {
   int seen = 0;
   for (int base = 0; base < pool && seen < want; base += kTile) {   // uniform over the block
-    const uint32_t m = free_bits(refcount, pool, base);
+    uint32_t m = free_bits(refcount, pool, base);
     const int n = __popc(m);
     int total;
     int rank = seen + block_incl_scan(n, part, total) - n;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      if ((m >> i) & 1u) {
-        if (rank < want) take(rank, base + int(threadIdx.x) * kPerThread + i);
-        ++rank;
-      }
-    }
+    for (; m != 0 && rank < want; m &= m - 1, ++rank) take(rank, base + int(threadIdx.x) * kPerThread + __ffs(m) - 1);
     seen += total;
   }
+  return min(seen, want);
 }
 
 // ------------------------------------------------------------------ resize
@@ -130,7 +122,6 @@ __global__ void __launch_bounds__(kThreads) pages_resize_kernel(ResizeArgs a) {
   pdl_launch_dependents();
   extern __shared__ int32_t upto[];              // [B]: pages needed by rows 0 .. b
   __shared__ int part[kWarps];
-  __shared__ int served_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   for (int b = warp; b < a.B; b += kWarps) {     // a warp per row: give back
@@ -164,36 +155,37 @@ __global__ void __launch_bounds__(kThreads) pages_resize_kernel(ResizeArgs a) {
     all += total;
   }
   if (all == 0) return;
-  const int free_pages = count_free(a.refcount, a.pool, part);
-  // rows are served as long as their needs and those of the rows before them fit
-  if (threadIdx.x == 0) served_s = all;
-  __syncthreads();
-  if (all > free_pages) {
-    if (threadIdx.x == 0) {
-      int lo = 0, hi = a.B;                      // rows [0, lo) fit
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (upto[mid] <= free_pages) lo = mid + 1; else hi = mid;
-      }
-      served_s = lo > 0 ? upto[lo - 1] : 0;
-      set_status(MD_DEV_NO_PAGES);
-    }
-    __syncthreads();
-  }
-  const int served = served_s;
-  take_lowest_free(a.refcount, a.pool, served, part, [&](int rank, int page) {
-    int lo = 0, hi = a.B - 1;                    // the first row whose running need exceeds the rank
+  auto row_of = [&](int rank) -> int {           // the first row whose running need exceeds the rank
+    int lo = 0, hi = a.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
       if (upto[mid] > rank) hi = mid; else lo = mid + 1;
     }
-    const int before = lo > 0 ? upto[lo - 1] : 0;
-    a.table[size_t(lo) * a.max_pages + a.n_pages[lo] + (rank - before)] = page;
+    return lo;
+  };
+  auto before = [&](int b) { return b > 0 ? upto[b - 1] : 0; };
+  const int found = take_lowest_free(a.refcount, a.pool, all, part, [&](int rank, int page) {
+    const int b = row_of(rank);
+    a.table[size_t(b) * a.max_pages + a.n_pages[b] + (rank - before(b))] = page;
     a.refcount[page] = 1;
   });
   __syncthreads();
+  // rows are served as long as their needs and those of the rows before them fit:
+  // the first that does not gives back what it got
+  int served = found;
+  if (found < all) {
+    const int b = row_of(found);
+    served = before(b);
+    int32_t* row = a.table + size_t(b) * a.max_pages + a.n_pages[b];
+    for (int i = threadIdx.x; i < found - served; i += kThreads) {
+      a.refcount[row[i]] = 0;
+      row[i] = -1;
+    }
+    if (threadIdx.x == 0) set_status(MD_DEV_NO_PAGES);
+  }
+  __syncthreads();
   for (int b = threadIdx.x; b < a.B; b += kThreads) {
-    const int need = upto[b] - (b > 0 ? upto[b - 1] : 0);
+    const int need = upto[b] - before(b);
     if (need > 0 && upto[b] <= served) a.n_pages[b] += need;
   }
 }
@@ -271,12 +263,12 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(ForkArgs a) {
   const int incl = block_incl_scan(need, part, total);
   if (total > 0) {
     if (need) s_owner[incl - 1] = i;
-    const int free_pages = count_free(a.refcount, a.pool, part);
-    if (total > free_pages && threadIdx.x == 0) set_status(MD_DEV_NO_PAGES);
-    take_lowest_free(a.refcount, a.pool, min(total, free_pages), part, [&](int rank, int page) {
+    __syncthreads();
+    const int found = take_lowest_free(a.refcount, a.pool, total, part, [&](int rank, int page) {
       s_fresh[s_owner[rank]] = page;
       a.refcount[page] = 1;
     });
+    if (found < total && threadIdx.x == 0) set_status(MD_DEV_NO_PAGES);
   }
   __syncthreads();
   const bool empty = !valid || len < 0 || (need && s_fresh[i] < 0);   // an idle source, or no page left
@@ -318,20 +310,34 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(ForkArgs a) {
 }
 
 // Copies the first `rows` slots of a fork's last page, every layer and head of
-// K and V. A head's slots of a page are contiguous: `rows` * dh elements.
-// One CTA per (layer and head, K or V, fork); traffic 4 * rows * dh B each.
-__global__ void __launch_bounds__(256) pages_fork_copy_kernel(uint4* k_pages, uint4* v_pages, const ForkJob* jobs, int pool,
-                                                              int Hkv, int page, int row16) {
+// K and V. A head's slots of a page are contiguous: `rows` * dh elements, four
+// 16-byte loads of a thread in flight (a page of 64 slots of 128 in one round).
+// One CTA per (kCopyHeads layers' heads, K or V, fork); bytes-bound, 4 * rows * dh B
+// a head read and written.
+constexpr int kCopyThreads = 256, kCopyLoads = 4, kCopyHeads = 4;
+
+__global__ void __launch_bounds__(kCopyThreads) pages_fork_copy_kernel(uint4* k_pages, uint4* v_pages, const ForkJob* jobs,
+                                                                       int layers, int pool, int Hkv, int page, int row16) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const ForkJob job = jobs[blockIdx.z];
   if (job.rows == 0) return;
-  const int layer = blockIdx.x / Hkv, hk = blockIdx.x - layer * Hkv;
   uint4* base = blockIdx.y ? v_pages : k_pages;
-  const uint4* from = base + ((size_t(layer) * pool + job.from) * Hkv + hk) * page * row16;
-  uint4* to = base + ((size_t(layer) * pool + job.to) * Hkv + hk) * page * row16;
-  const int n = job.rows * row16;
-  for (int i = threadIdx.x; i < n; i += 256) to[i] = from[i];
+  const int n = job.rows * row16, heads = layers * Hkv;
+  for (int lh = blockIdx.x * kCopyHeads; lh < min(heads, int(blockIdx.x + 1) * kCopyHeads); ++lh) {
+    const int layer = lh / Hkv, hk = lh - layer * Hkv;
+    const uint4* from = base + ((size_t(layer) * pool + job.from) * Hkv + hk) * page * row16;
+    uint4* to = base + ((size_t(layer) * pool + job.to) * Hkv + hk) * page * row16;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kCopyLoads * kCopyThreads) {
+      uint4 x[kCopyLoads];
+#pragma unroll
+      for (int k = 0; k < kCopyLoads; ++k)
+        if (i0 + k * kCopyThreads < n) x[k] = from[i0 + k * kCopyThreads];
+#pragma unroll
+      for (int k = 0; k < kCopyLoads; ++k)
+        if (i0 + k * kCopyThreads < n) to[i0 + k * kCopyThreads] = x[k];
+    }
+  }
 }
 
 }  // namespace pages
