@@ -411,19 +411,23 @@ def tree_commit(k_cache, v_cache, tree: Tree, prefix_len, accept_len, path, bonu
 _I64x9 = ctypes.c_int64 * 9
 
 
-def _refuse(what, t, name, dtype, shape, dev):
-    """Raises for the first thing wrong with a tensor (_ptrs found something)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: {name}: expected a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: {name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: {name}: must be a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: {name}: must be contiguous")
-    raise ValueError(f"{what}: {name} is on cuda:{t.get_device()}, expected cuda:{dev}")
+def _refuse(what, dev, specs):
+    """Raises for what is wrong with a call's tensors (_ptrs found something):
+    types and shapes first, then where they live."""
+    for t, name, dtype, shape in specs:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what}: {name}: expected a torch.Tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{what}: {name}: expected {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    for t, name, _, _ in specs:
+        if not t.is_cuda:
+            raise ValueError(f"{what}: {name}: must be a CUDA tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name}: must be contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: {name} is on cuda:{t.get_device()}, expected cuda:{dev}")
 
 
 def _ptrs(what, dev, *specs):
@@ -437,7 +441,7 @@ def _ptrs(what, dev, *specs):
         except AttributeError:
             ok = False
         if not ok:
-            _refuse(what, t, name, dtype, shape, dev)
+            _refuse(what, dev, specs)
         out.append(t.data_ptr())
     return out
 
@@ -514,7 +518,8 @@ def _head_rows(what, t, name, dev, shape):
     """Pointer and element strides (request, token, head) of a [B,T,H,dh] view
     whose last dimension is contiguous."""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev or dev < 0:
-        _refuse(what, t, name, torch.bfloat16, shape, dev)
+        _refuse(what, dev, [(t, name, torch.bfloat16, shape)])
+        raise ValueError(f"{what}: {name}: must be a CUDA tensor of the call's device")
     sb, st, sh, sd = t.stride()
     B, T, H, _ = shape
     # a dimension of size 1 is never stepped over: its stride may be anything

@@ -941,12 +941,13 @@ struct PagedAttnPlan {
 // one tile, 1.1 if other tiles' CTAs read the same keys from L2, 1.75 for two, twice
 // that for fp32 results (one score buffer, three P V products); CTAs
 // past one wave fill the SMs as they come, with half a CTA's time left uneven; and
-// no call is faster than its keys' bytes from memory. Chunks are counted by
-// what the table can hold: the lengths are on the device.
+// no call is faster than its keys' bytes from memory, 1.1 times that in one wave (a
+// batch's lengths differ, and its longest request then keeps one CTA). Chunks are
+// counted by what the table can hold: the lengths are on the device.
 //   70B tree, B = 1 (40 tiles, 33 chunks): one tile, 3 splits 23.7 us; two tiles, 5
 //     splits 26.7. B = 8: one tile 124, two tiles 113.6.
 //   Decoding, 8 KV heads, 4096 slots: 1 split 32.9, 4 15.3, 8 12.5, 12 (two waves)
-//     22.6. 16 requests of 26000: 1 split 261, 2 276.
+//     22.6. 16 requests of 26000: 1 split 261, 2 276; of 20001 to 32768: 316, 270.
 PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, int max_pages, bool f32) {
   PagedAttnPlan p;
   const int G = Hq / Hkv;
@@ -973,7 +974,8 @@ PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, i
       const double longest = tpu == 2 ? two : one;
       const double all = tpu == 2 ? (tiles / 2) * two + (tiles % 2) * one : tiles * one;   // a KV head's units, one split
       const bool waves = base * s > slots;
-      const double us = std::max(waves ? double(B) * Hkv * s * all / slots + 0.5 * longest : longest, bytes_us + 8.0);
+      double us = waves ? double(B) * Hkv * s * all / slots + 0.5 * longest : longest;
+      if (us < bytes_us + 8.0) us = (bytes_us + 8.0) * (waves || B == 1 ? 1.0 : 1.1);
       if (best == 0 || us < best) {
         best = us;
         p.tpu = tpu;

@@ -535,3 +535,74 @@ def test_fork_leaves_out_what_cannot_be():
     status, g = call([0], [3], ref=np.array([1, 1, 1, 1, 1, 1], dtype=np.int32))     # no page left: row 3 stays empty
     assert status == md.binding.DEV_NO_PAGES and g[5].cpu().tolist()[3] == -1 and g[3].cpu().tolist()[3] == 0
     assert g[4].cpu().tolist() == [1, 1, 1, 1, 1, 1]
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    """Attention calls of two streams at once, and one call's result on a side stream."""
+    rng = np.random.default_rng(21)
+    parent, rank = _tree(16)
+    T, Hq, Hkv, dh, page, P = 17, 8, 2, 128, 32, [900, 33]
+    table, pool = _table(rng, P, T, page)
+    q = bf16_tensor(gen.normal_bf16(2, "q", (2, T, Hq, dh), 1.0))
+    kp = bf16_tensor(gen.normal_bf16(2, "k_cache", (pool, Hkv, page, dh), 1.0))
+    vp = bf16_tensor(gen.normal_bf16(2, "v_cache", (pool, Hkv, page, dh), 1.0))
+    tb, Pd = i32(table), i32(P)
+    want = _attention(q, kp, vp, tb, Pd, parent, rank, torch.bfloat16)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.zeros_like(want) for _ in range(8)] for _ in streams]
+    wss = [md.workspace(md.attention_paged_workspace_bytes(2, T, Hq, Hkv, dh, page, table.shape[1])) for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for s, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                _attention(q, kp, vp, tb, Pd, parent, rank, torch.bfloat16, ws=wss[s], out=outs[s][i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for per in outs for o in per) and md.device_status() == 0
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,page,P", [(40, 1, 8, 1, 16, (0, 700)), (70, 17, 8, 2, 32, (1, 300)), (24, 65, 8, 4, 64, (0, 400))])
+def test_more_units_than_one_wave(B, T, Hq, Hkv, page, P):
+    """Grids past one wave, requests taken from the longest down."""
+    rng = np.random.default_rng(B)
+    parent, rank = _tree(T - 1)
+    lens = [int(x) for x in rng.integers(P[0], P[1], B)]
+    lens[3] = -1
+    table, pool = _table(rng, lens, T, page)
+    q = gen.normal_bf16(4, "q", (B, T, Hq, 64), 1.0)
+    kp = gen.normal_bf16(4, "k_cache", (pool, Hkv, page, 64), 1.0)
+    vp = gen.normal_bf16(4, "v_cache", (pool, Hkv, page, 64), 1.0)
+    out = _attention(bf16_tensor(q), bf16_tensor(kp), bf16_tensor(vp), i32(table), i32(lens), parent, rank, torch.bfloat16)
+    assert md.device_status() == 0
+    _check_attention(out, q, kp, vp, table, lens, parent)
+
+
+def test_scores_far_apart_and_rows_of_nan():
+    """Maxima that climb by thousands from chunk to chunk (the running maximum moves,
+    the result is rescaled), a prefix key of NaN, and a query of NaN."""
+    T, Hq, Hkv, dh, page, P = 1, 4, 2, 64, 16, [1000, 1000, 1000]
+    rng = np.random.default_rng(8)
+    table, pool = _table(rng, P, T, page)
+    q = gen.normal_bf16(5, "q", (3, T, Hq, dh), 1.0)
+    kf = bf16_to_f64(gen.normal_bf16(5, "k_cache", (pool, Hkv, page, dh), 1.0))
+    for b in range(3):
+        for i, pg in enumerate(table[b]):
+            kf[pg] *= 1.0 + 2.0 * i if pg >= 0 else 1.0
+    kp = to_bits(torch.from_numpy(kf).to(torch.bfloat16))
+    vp = gen.normal_bf16(5, "v_cache", (pool, Hkv, page, dh), 1.0)
+    kp[table[1, 5], 0, 3] = NAN                            # KV head 0 of request 1
+    q[2, 0, 1] = NAN                                       # query head 1 of request 2
+    for dtype in (torch.float32, torch.bfloat16):
+        out = _attention(bf16_tensor(q), bf16_tensor(kp), bf16_tensor(vp), i32(table), i32(P), [-1], [0], dtype)
+        nan = torch.isnan(out).all(dim=-1).cpu().numpy()
+        want = np.zeros_like(nan)
+        want[1, 0, :2] = True
+        want[2, 0, 1] = True
+        assert np.array_equal(nan, want) and np.array_equal(torch.isnan(out).any(dim=-1).cpu().numpy(), want)
+        ref = op.tree_attention_paged(q, kp, vp, table, P, [-1])
+        absv = op.tree_attention_paged(q, kp, vp & 0x7FFF, table, P, [-1])
+        got = out.float().cpu().numpy()
+        # scores of up to 64 * 127 * 3.5^2 / 8 in fp32: off by 2^-24 of that and of their products' sum
+        wide = 2.0 ** -7
+        tol = 2 * (wide + 2.0 ** -8) * absv + 2.0 ** -8 * np.abs(ref)
+        assert (np.abs(got - ref) <= tol)[~want].all()

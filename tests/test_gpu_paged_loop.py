@@ -1,0 +1,136 @@
+"""The paged step as a server uses it, against the oracle running the same loop:
+prompts of different lengths appended, steps of heads, tree, append in two
+layers, attention, acceptance, commit and trim, a sequence forked into an idle
+row, a request leaving, and the last step captured in a CUDA graph.
+
+The oracle follows the GPU's written keys bit for bit (each checked against the
+fp64 rotation first), so that attention is compared on the same cache.
+"""
+import numpy as np
+import pytest
+
+import medusa_draft_heads_b200 as md
+from medusa_draft_heads_b200.step import PagedMedusaStep
+from oracle import accept as oacc
+from oracle import heads as oh
+from oracle import paged as op
+from oracle import tree as ot
+from oracle.heads import bf16_to_f64
+from seeded_inputs import gen, synth
+from seeded_inputs.workloads import TREE_ACCEPT
+
+from .helpers import bf16_tensor, f32, i32, to_bits
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def test_paged_decode_loop_matches_oracle():
+    B, d, V, K, kph, n = 4, 256, 2048, 4, (4, 3, 2, 2), 16
+    Hq, Hkv, dh, page, width, pool, layers = 4, 2, 64, 16, 8, 24, 2
+    T = n + 1
+    parent, rank, _ = ot.spec_from_tuples(ot.select_tree(kph, TREE_ACCEPT, n))
+    step = PagedMedusaStep(B=B, M=B, d=d, V=V, K=K, k_per_head=kph, tree_tuples=md.select_tree(kph, TREE_ACCEPT, n), Hq=Hq,
+                           Hkv=Hkv, dh=dh, page_size=page, max_pages=width, pool_pages=pool, out_dtype=torch.bfloat16)
+    W1, b1, Wv = (gen.normal_bf16(0, s, sh, 0.02) for s, sh in (("W1", (K, d, d)), ("b1", (K, d)), ("Wv", (K, d, V))))
+    gW = [bf16_tensor(x) for x in (W1, b1, Wv)]
+    qn, kn = gen.normal_bf16(0, "q", (dh,), 1.0), gen.normal_bf16(1, "q", (dh,), 1.0)
+    freq = (10000.0 ** (-np.arange(dh // 2) / (dh // 2))).astype(np.float32)
+    k = np.full((layers, pool, Hkv, page, dh), 0x7FC0, dtype=np.uint16)       # the pools start as NaN
+    v = k.copy()
+    gk, gv = bf16_tensor(k), bf16_tensor(v)
+    table, cnt, ref = np.full((B, width), -1, np.int32), np.zeros(B, np.int32), np.zeros(pool, np.int32)
+
+    def pages_equal():
+        for got, want in ((step.block_table, table), (step.n_pages, cnt), (step.refcount, ref)):
+            assert np.array_equal(got.cpu().numpy(), want)
+
+    def append(seed, width_t, pos, prefix, n_new, q_out=None):
+        """Both layers' new tokens on the GPU; the oracle's pools take the checked bits."""
+        outs = []
+        for layer in range(layers):
+            qkv = gen.normal_bf16(seed + layer, "q", (B, width_t, Hq + 2 * Hkv, dh), 1.0)
+            gq, gkk, gvv = bf16_tensor(qkv).split([Hq, Hkv, Hkv], dim=2)
+            out = torch.zeros((B, width_t, Hq, dh), dtype=torch.bfloat16, device="cuda")
+            step.append(gq, gkk, gvv, i32(pos), torch.from_numpy(freq).cuda(), gk[layer], gv[layer], i32(prefix),
+                        q_norm=bf16_tensor(qn), k_norm=bf16_tensor(kn), n_new=None if n_new is None else i32(n_new), q_out=out)
+            _, written = op.qk_rope_append(qkv[:, :, :Hq], qkv[:, :, Hq:Hq + Hkv], qkv[:, :, Hq + Hkv:], pos, freq, table, prefix,
+                                           k[layer].shape, qn, kn, 1e-6, False, n_new)
+            bits = to_bits(gk[layer])
+            for (pg, row), (kr, vr) in written.items():
+                got = bf16_to_f64(bits[pg, :, row])
+                assert (np.abs(got - kr) <= 2.0 ** -8 * np.abs(kr) + 2.0 ** -20 * np.abs(kr).max()).all()
+                k[layer, pg, :, row], v[layer, pg, :, row] = bits[pg, :, row], vr
+            assert np.array_equal(bits, k[layer]) and np.array_equal(to_bits(gv[layer]), v[layer])
+            outs.append(out)
+        return outs
+
+    # ---- prompts: 37, 16 and 5 tokens; row 3 is idle ----
+    lens = np.array([37, 16, 5, -1], dtype=np.int32)
+    step.prefill_pages(i32(lens))
+    table, cnt, ref, _ = op.pages_resize(table, cnt, ref, lens, page)
+    pages_equal()
+    start = np.where(lens < 0, -1, 0).astype(np.int32)
+    append(50, 40, np.tile(np.arange(40), (B, 1)), start, np.maximum(lens, 0))
+    P = lens.copy()
+    root = synth.root_tokens(0, B, V)
+    for s in range(3):
+        seed = 100 + 10 * s
+        if s == 1:                                        # row 0 goes on twice; row 2 leaves
+            P[2] = -1
+            gP = i32(P)
+            step.prefill_pages(gP)
+            table, cnt, ref, _ = op.pages_resize(table, cnt, ref, P, page)
+            step.fork(gk, gv, i32([0, -1]), i32([3, 0]), gP)
+            k, v, table, cnt, ref, P = op.pages_fork(k, v, table, cnt, ref, np.array([0, -1]), np.array([3, 0]), P)
+            root[3] = root[0]
+            assert gP.cpu().tolist() == P.tolist()
+            assert np.array_equal(to_bits(gk), k) and np.array_equal(to_bits(gv), v)
+            pages_equal()
+        gP, groot = i32(P), i32(root)
+        h = gen.normal_bf16(seed, "h", (B, d), 1.0)
+        rid, _, _, _ = oh.medusa_heads(h, W1, b1, Wv, kph)
+        live = [b for b in range(B) if P[b] >= 0]
+        rtok, _, _, rpos = ot.tree_build(parent, rank, rid, root, P)
+        step.heads(bf16_tensor(h), *gW)
+        step.build(groot, gP)
+        assert np.array_equal(step.tokens.cpu().numpy()[live], rtok[live])
+        assert np.array_equal(step.pos.cpu().numpy()[live], rpos[live])
+        step.reserve(gP)
+        table, cnt, ref, short = op.pages_resize(table, cnt, ref, P, page, T)
+        assert not short
+        pages_equal()
+        qs = append(seed, T, rpos, P, None)
+        for layer in range(layers):
+            step.attention(qs[layer], gk[layer], gv[layer], gP)
+            q = to_bits(qs[layer])
+            want = op.tree_attention_paged(q, k[layer], v[layer], table, P, parent)
+            absv = op.tree_attention_paged(q, k[layer], v[layer] & 0x7FFF, table, P, parent)
+            got = step.attn_out.float().cpu().numpy()
+            assert (np.abs(got - want) <= 2 * (2.0 ** -13 + 2.0 ** -8) * absv + 2.0 ** -8 * np.abs(want)).all()
+        logits = synth.planted_logits(seed, parent, rtok, V, TREE_ACCEPT)
+        L, path, bonus, _ = oacc.greedy_accept(logits, rtok, parent, K)
+        glog = f32(logits)
+        if s < 2:
+            step.accept(glog)
+            step.commit(gk, gv, gP)
+            step.trim()
+        else:                                             # the tail of the step from a graph
+            state = gk.view(torch.int16), gv.view(torch.int16), step.block_table, step.n_pages, step.refcount
+            before = [x.clone() for x in state]
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                step.accept(glog)
+                step.commit(gk, gv, gP)
+                step.trim()
+            assert all(torch.equal(a, b) for a, b in zip(before, state))     # nothing ran yet
+            g.replay()
+        k, v, P2, root2, _ = op.tree_commit_paged(k, v, table, P, L, path, bonus, T)
+        assert np.array_equal(to_bits(gk), k) and np.array_equal(to_bits(gv), v)
+        assert step.new_prefix_len.cpu().tolist() == P2.tolist() and step.next_root.cpu().tolist() == root2.tolist()
+        table, cnt, ref, _ = op.pages_resize(table, cnt, ref, P2, page)
+        pages_equal()
+        assert md.device_status() == 0
+        P, root = P2.astype(np.int32), np.maximum(root2, 0).astype(np.int32)
+    # the fork's sequences went on in pages of their own, sharing the first
+    assert ref.max() == 2 and table[0, 0] == table[3, 0] and table[0, 2] != table[3, 2]
