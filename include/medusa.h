@@ -533,8 +533,10 @@ MD_API md_status md_attention_paged_workspace(int32_t B, int32_t T, int32_t Hq, 
  *         MD_DEV_BAD_PREFIX and writes zeros for that request. A bad page is
  *         read as zeros.
  * scale   softmax scale; 0 means 1/sqrt(dh).
- * out     [B, T, Hq, dh] fp32 (MD_OUT_F32; weights kept to about 16 bits, as in
- *         md_tree_attention) or bf16 (MD_OUT_BF16; weights rounded to bf16).
+ * out     [B, T, Hq, dh] fp32 (MD_OUT_F32; weights kept to 24 bits, sums of at most
+ *         1024 keys in the tensor cores up to 32768 slots: off by a few 1e-6 of the
+ *         result there, less where shorter) or bf16 (MD_OUT_BF16; weights rounded to
+ *         bf16, about twice as fast over long prefixes).
  * q, k_pages, v_pages and out 16-byte aligned. The workspace is
  * md_attention_paged_workspace()'s, 256-byte aligned, with any contents.
  * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_WORKSPACE, MD_ERR_CUDA. */

@@ -7,44 +7,53 @@
 // block_table[b, s / page]. The T * G query rows (node, head of the group) of a
 // KV head share its keys, so scores and weighted sums are dense products.
 //
-// CTA = (KV split, unit of up to two 128-row tiles, KV head, request). It walks
-// its chunks of 128 keys with two softmax warpgroups, each with a stream of its
-// own: S (128 columns of TMEM, overwritten in place by the weights P) and O
-// (DH columns).
-//   - two tiles: stream w is row tile w, and both walk every chunk, so a chunk
-//     fetched once serves 256 rows;
-//   - one tile (a request with few rows: decoding, chains, the odd last tile):
-//     the streams take the chunks in turn and are joined at the end.
-// While one stream's warps run its softmax the tensor cores work for the other.
+// CTA = (KV split, unit of one or two 128-row tiles, KV head, request). Two streams,
+// each with scores S, weights P (written over S) and an accumulator O in TMEM, walk
+// the split's keys in jobs of 64:
+//   - two tiles: stream w is row tile w and takes every job, so that a chunk of
+//     keys fetched once serves 256 rows;
+//   - one tile (decoding, chains, the odd last tile, or where more CTAs pay): the
+//     streams take the jobs in turn and are joined at the end.
+// While one stream's warps run a job's softmax the tensor cores work for the other,
+// and (bf16 results) for this stream's next job, whose S goes to a second buffer.
 //
-//   warp 0      K: one TMA copy per page piece and 64-column block, each lane a
-//               piece (its page id from the block table), three slots
-//   warp 1      one thread issues, per (stream, chunk): O += P V, then the
-//               stream's next S = Q K^T. A stream's S landing implies that its
-//               previous P V landed too (they complete in issue order), so the
-//               softmax may rescale O in place.
-//   warp 2      V, as K; two slots, a third where the second Q tile would be
-//   warp 3      the Q tiles
-//   warps 4-11  softmax: thread = row. Running maximum m (moved only when a
-//               chunk exceeds it by 2^8, O and the sum then rescaled), weights
-//               P = exp2(S - m), their sum in fp32.
+//   warp 0      K: chunks of 128 keys, one TMA copy per page piece and 64-column
+//               block, each lane a piece (its page id from the block table)
+//   warp 2      V, as K; then the look at the chunks that reach the tree (below)
+//   warps 1, 3  MMAs of stream 0 and 1 (warp 3 also fetches the Q tiles): O += P V
+//               of a job, then S = Q K^T of the next one in its buffer. Both take
+//               their operands in issue order, so S may overwrite P behind its P V.
+//   warps 4-19  softmax: a row of a stream is two threads, 32 keys of a job each;
+//               they exchange maxima through shared memory. The reference maximum m
+//               moves only when a job exceeds it by 2^8: O and the sum are then
+//               rescaled in place, once the stream's last P V has landed. P =
+//               exp2(S - m); sums in fp32.
 //
-// P is rounded to bf16 for the product with V (the relative error of a weight,
-// 2^-9, averages out over the keys, and the bf16 output is rounded to the same
-// precision). For fp32 outputs P is split into hi + lo bf16 parts (to 2^-14) and
-// P V runs twice.
+// P is rounded to bf16 for the product with V where the result is bf16: the error of
+// a weight, 2^-9 on average less, averages out over the keys, and the result is
+// rounded to the same precision (0.0023 of the result against 64 bits, 0.0017 being
+// the last rounding's own). For fp32 results P is three bf16 parts, 24 bits, and P V
+// three products; S then has one buffer, the parts needing the other's columns.
 //
 // The KV splits of a unit are the CTAs of a cluster: O and (m, sum) of every
 // stream are staged in shared memory, and each CTA combines its share of the
 // rows from all of them (distributed shared memory). Splits are made of the
-// request's own length on the device, so a table wider than the sequences
-// costs nothing.
+// request's own length on the device, so a table wider than the sequences costs
+// little.
 //
 // Slots behind the tree's last hold anything, NaN included: their scores are
 // replaced, and their V rows zeroed in shared memory (0 * NaN would reach O). A
 // tree node's V that is not finite must reach only the rows that see the node:
 // such elements are zeroed in shared memory too and added to those rows'
 // results at the end.
+//
+// What bounds it. Long prefixes with few rows: bytes (16 requests of 20k to 33k
+// slots, one node: 266 us, 6.3 TB/s, 97 % of a copy's rate). Many rows: the two-tile
+// walk takes 1.76 us a chunk of 128 keys where its tensor work takes 1.34 (measured
+// without the softmax: S with N = 64 is held back by shared memory, 43 clocks an MMA
+// against 32) and the special-function unit 1.08; 70B batch of 8: 103 us, 0.66
+// PFLOP/s. One request: set-up, first loads, the splits' joining and the launch,
+// about 8 us, are as much as the walk (70B tree over 4096 slots: 23.6 us).
 #pragma once
 
 #include "common.cuh"
