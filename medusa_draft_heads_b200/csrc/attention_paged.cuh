@@ -29,8 +29,8 @@
 //               rescaled in place, once the stream's last P V has landed. P =
 //               exp2(S - m); sums in fp32.
 //
-// P is rounded to bf16 for the product with V where the result is bf16: the error of
-// a weight, 2^-9 on average less, averages out over the keys, and the result is
+// P is rounded to bf16 for the product with V where the result is bf16: a weight's
+// error, at most 2^-8 of it either way, averages out over the keys, and the result is
 // rounded to the same precision (0.0023 of the result against 64 bits, 0.0017 being
 // the last rounding's own). For fp32 results P is three bf16 parts, 24 bits, and P V
 // three products; S then has one buffer, the parts needing the other's columns.
@@ -146,6 +146,15 @@ __device__ __forceinline__ void settle(float* v) {
   asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
 
+// 4-D tiled TMA load (no multicast).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
 // 16 columns, loaded and stored (few registers beside a row of scores).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   asm volatile(
@@ -225,28 +234,40 @@ __device__ __forceinline__ uint64_t visible_bits(uint64_t lo, uint64_t hi, int n
 
 __device__ __forceinline__ bool bf16_finite(uint32_t v) { return (v & 0x7F80u) != 0x7F80u; }
 
+// Where the page piece of this lane lies for the chunk at key0: its page's row of the
+// tensor map and its first slot in the page. Loaded a chunk ahead of its use.
+struct Piece {
+  int page, at;
+};
+__device__ __forceinline__ Piece piece_of(const int32_t* row, int key0, int nkeys, const Args& a) {
+  const int key = key0 + int(threadIdx.x & 31) * a.piece;
+  Piece p = {0, 0};
+  if (key < min(nkeys, key0 + kBN)) {
+    const int pi = key / a.page;
+    p.page = row[pi];
+    p.at = key - pi * a.page;
+  }
+  return p;
+}
+
 // The copies of one chunk of K or V into a ring slot, each lane a page piece.
 // Pieces behind the last slot are not copied. All lanes of a warp call it.
 template <int DH, bool F32>
-__device__ __forceinline__ void load_chunk(uint32_t dst, const CUtensorMap* map, uint32_t bar, const int32_t* row, int key0,
-                                           int nkeys, int hk, const Args& a) {
+__device__ __forceinline__ void load_chunk(uint32_t dst, const CUtensorMap* map, uint32_t bar, Piece p, int key0, int nkeys,
+                                           int hk, const Args& a) {
   using C = Cfg<DH, F32>;
   const int lane = threadIdx.x & 31;
-  const int left = min(kBN, nkeys - key0);
-  const int pieces = (left + a.piece - 1) / a.piece;
+  const int pieces = (min(kBN, nkeys - key0) + a.piece - 1) / a.piece;
   if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(pieces * a.piece) * DH * 2);
   __syncwarp();
   if (lane < pieces) {
-    const int key = key0 + lane * a.piece;
-    const int pi = key / a.page;
-    int pg = row[pi];
-    if (pg < 0 || pg >= a.pool) {
+    if (p.page < 0 || p.page >= a.pool) {
       set_status(MD_DEV_BAD_PAGE);
-      pg = a.pool;                       // past the pool: the copy fills zeros
+      p.page = a.pool;                   // past the pool: the copy fills zeros
     }
 #pragma unroll
     for (int kb = 0; kb < C::KB; ++kb)
-      tma_load_3d(dst + kb * (kBN * 128) + lane * a.piece * 128, map, kb * 64, key - pi * a.page, pg * a.Hkv + hk, bar);
+      tma_load_3d(dst + kb * (kBN * 128) + lane * a.piece * 128, map, kb * 64, p.at, p.page * a.Hkv + hk, bar);
   }
 }
 
@@ -355,13 +376,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const int withhold = *const_cast<volatile int*>(&g_withhold_chunk);   // test hook, normally -1
     int n = 0;
+    Piece next = piece_of(trow, c_begin * kBN, nch > 0 ? nkeys : 0, a);
     for (int c = 0; c < nch; ++c) {
+      const int key0 = (c_begin + c) * kBN;
+      const Piece p = next;
+      if (c + 1 < nch) next = piece_of(trow, key0 + kBN, nkeys, a);
       if (c == withhold) continue;
       const int st = c % kKStages;
       if (c >= kKStages && !wait_phase(smem_u32(&k_empty[st]), ((c / kKStages) - 1) & 1)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      load_chunk<DH, F32>(smem_u32(sK + st * C::kTile), &kmap, smem_u32(&k_full[st]), trow, (c_begin + c) * kBN, nkeys, hk, a);
+      load_chunk<DH, F32>(smem_u32(sK + st * C::kTile), &kmap, smem_u32(&k_full[st]), p, key0, nkeys, hk, a);
       n = c + 1;
     }
     // every copy issued into this CTA's shared memory lands before it may exit
@@ -373,13 +398,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const int withhold = *const_cast<volatile int*>(&g_withhold_chunk);
     int n = 0;
+    Piece next = piece_of(trow, c_begin * kBN, nch > 0 ? nkeys : 0, a);
     for (int c = 0; c < nch; ++c) {
+      const int key0 = (c_begin + c) * kBN;
+      const Piece p = next;
+      if (c + 1 < nch) next = piece_of(trow, key0 + kBN, nkeys, a);
       if (c == withhold) continue;
       const int st = c % vst;
       if (c >= vst && !wait_phase(smem_u32(&v_empty[st]), ((c / vst) - 1) & 1)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      load_chunk<DH, F32>(smem_u32(v_slot(st)), &vmap, smem_u32(&v_full[st]), trow, (c_begin + c) * kBN, nkeys, hk, a);
+      load_chunk<DH, F32>(smem_u32(v_slot(st)), &vmap, smem_u32(&v_full[st]), p, key0, nkeys, hk, a);
       n = c + 1;
     }
     // V rows that P's zeros must not meet: slots behind the last key, and what is
@@ -433,8 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < tiles; ++i)
 #pragma unroll
           for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_3d(smem_u32(sQ + i * C::kQTile + kb * (kBM * 128)), &qmap, kb * 64, hk * a.G,
-                        b * T + tok0 + i * a.tpt, qb);
+            tma_load_4d(smem_u32(sQ + i * C::kQTile + kb * (kBM * 128)), &qmap, kb * 64, hk * a.G, tok0 + i * a.tpt, b, qb);
       }
       __syncwarp();
       bool ok = __all_sync(0xffffffffu, wait_phase(smem_u32(q_full), 0));

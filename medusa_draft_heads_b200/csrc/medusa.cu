@@ -1002,12 +1002,14 @@ md_status launch_attn_paged(const md::attn_paged::Args& a, const md_bf16* q, con
   EncodeTiledFn fn = encode_fn();
   if (!fn) return MD_ERR_CUDA;
   {
-    // q [B*T][Hq][dh]: a box holds a tile's nodes, the G heads of one KV head each
-    cuuint64_t dims[3] = {cuuint64_t(DH), cuuint64_t(a.Hq), cuuint64_t(a.B) * tree->tp.T};
-    cuuint64_t strides[2] = {cuuint64_t(DH) * 2, cuuint64_t(a.Hq) * DH * 2};
-    cuuint32_t box[3] = {64, cuuint32_t(a.G), cuuint32_t(a.tpt)};
-    cuuint32_t estr[3] = {1, 1, 1};
-    if (fn(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<md_bf16*>(q), dims, strides, box, estr,
+    // q [B][T][Hq][dh]: a box holds a tile's nodes, the G heads of one KV head each; rows
+    // past the last node come as zeros, which the tensor cores multiply at less power
+    // (decoding runs into the power cap on the rows it does not need)
+    cuuint64_t dims[4] = {cuuint64_t(DH), cuuint64_t(a.Hq), cuuint64_t(tree->tp.T), cuuint64_t(a.B)};
+    cuuint64_t strides[3] = {cuuint64_t(DH) * 2, cuuint64_t(a.Hq) * DH * 2, cuuint64_t(tree->tp.T) * a.Hq * DH * 2};
+    cuuint32_t box[4] = {64, cuuint32_t(a.G), cuuint32_t(a.tpt), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    if (fn(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<md_bf16*>(q), dims, strides, box, estr,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return MD_ERR_CUDA;
