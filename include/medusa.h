@@ -85,7 +85,8 @@ enum {
  *   tree:      1 <= T <= 128, depth <= K.
  *   attention: dh in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 16.
  *   paged:     as attention; page_size % 16 == 0 for md_tree_attention_paged,
- *              any page_size >= 1 for the other calls; B <= 65535.
+ *              any page_size >= 1 for the other calls; B <= 65535; max_pages *
+ *              page_size, B * max_pages and pool_pages * Hkv within int32.
  */
 #define MD_MAX_T 128
 #define MD_MAX_K 8
@@ -537,7 +538,7 @@ MD_API md_status md_attention_paged_workspace(int32_t B, int32_t T, int32_t Hq, 
  *         1024 keys in the tensor cores up to 32768 slots: off by a few 1e-6 of the
  *         result there, less where shorter) or bf16 (MD_OUT_BF16; weights rounded to
  *         bf16, about twice as fast over long prefixes).
- * q, k_pages, v_pages and out 16-byte aligned. The workspace is
+ * q, k_pages, v_pages and out 16-byte aligned; out not q. The workspace is
  * md_attention_paged_workspace()'s, 256-byte aligned, with any contents.
  * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_WORKSPACE, MD_ERR_CUDA. */
 MD_API md_status md_tree_attention_paged(const md_bf16* q, const md_bf16* k_pages, const md_bf16* v_pages,

@@ -409,13 +409,17 @@ def tree_commit(k_cache, v_cache, tree: Tree, prefix_len, accept_len, path, bonu
 # ---------------------------------------------------------------------------
 
 _I64x9 = ctypes.c_int64 * 9
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_Tensor = torch.Tensor
+_NONE = (None, None, None, None)   # stands for an optional tensor left out
 
 
 def _refuse(what, dev, specs):
     """Raises for what is wrong with a call's tensors (_ptrs found something):
     types and shapes first, then where they live."""
+    specs = [s for s in specs if s is not _NONE]
     for t, name, dtype, shape in specs:
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, _Tensor):
             raise TypeError(f"{what}: {name}: expected a torch.Tensor")
         if t.dtype != dtype:
             raise TypeError(f"{what}: {name}: expected {dtype}, got {t.dtype}")
@@ -436,6 +440,9 @@ def _ptrs(what, dev, *specs):
     reads; _refuse finds the words for one that fails."""
     out = []
     for t, name, dtype, shape in specs:
+        if t is None and name is None:   # an argument left out
+            out.append(None)
+            continue
         try:
             ok = t.dtype is dtype and t.get_device() == dev >= 0 and t.shape == shape and t.is_contiguous()
         except AttributeError:
@@ -448,7 +455,7 @@ def _ptrs(what, dev, *specs):
 
 def _dims(what, t, name, n):
     """The shape of a tensor with n dimensions."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{what}: {name}: expected a torch.Tensor")
     if t.dim() != n:
         raise ValueError(f"{what}: {name}: expected {n} dims, got {t.dim()}")
@@ -457,7 +464,7 @@ def _dims(what, t, name, n):
 
 def _pool_dims(what, t):
     """(layers, pool_pages, Hkv, page_size, dh) of a pool of one layer or of a stack."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{what}: k_pages: expected a torch.Tensor")
     if t.dim() not in (4, 5):
         raise ValueError(f"{what}: k_pages: expected 4 or 5 dims, got {t.dim()}")
@@ -500,25 +507,25 @@ def tree_attention_paged(q, k_pages, v_pages, block_table, prefix_len, tree: Tre
     if T != tree.T:
         raise ValueError(f"{what}: T has shape {T}, expected {tree.T}")
     out_dtype = getattr(out, "dtype", None)
-    if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
+    if out_dtype is not _F32 and out_dtype is not _BF16:
         raise TypeError(f"{what}: out: expected torch.float32 or torch.bfloat16, got {out_dtype}")
     dev = q.get_device()
     pool = (pages, Hkv, page, dh)
     qp, kp, vp, tp, lp, op, wp = _ptrs(
-        what, dev, (q, "q", torch.bfloat16, q.shape), (k_pages, "k_pages", torch.bfloat16, pool),
-        (v_pages, "v_pages", torch.bfloat16, pool), (block_table, "block_table", torch.int32, (B, width)),
-        (prefix_len, "prefix_len", torch.int32, (B,)), (out, "out", out_dtype, q.shape),
-        (ws, "ws", torch.uint8, getattr(ws, "shape", ())))
+        what, dev, (q, "q", _BF16, q.shape), (k_pages, "k_pages", _BF16, pool),
+        (v_pages, "v_pages", _BF16, pool), (block_table, "block_table", _I32, (B, width)),
+        (prefix_len, "prefix_len", _I32, (B,)), (out, "out", out_dtype, q.shape),
+        (ws, "ws", _U8, getattr(ws, "shape", ())))
     _launch("md_tree_attention_paged", lib().md_tree_attention_paged, dev, stream, qp, kp, vp, pages, page, tp, width, lp,
-            tree.handle, B, Hq, Hkv, dh, scale, op, MD_OUT_BF16 if out_dtype is torch.bfloat16 else MD_OUT_F32, wp,
+            tree.handle, B, Hq, Hkv, dh, scale, op, MD_OUT_BF16 if out_dtype is _BF16 else MD_OUT_F32, wp,
             ws.numel())
 
 
 def _head_rows(what, t, name, dev, shape):
     """Pointer and element strides (request, token, head) of a [B,T,H,dh] view
     whose last dimension is contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev or dev < 0:
-        _refuse(what, dev, [(t, name, torch.bfloat16, shape)])
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev or dev < 0:
+        _refuse(what, dev, [(t, name, _BF16, shape)])
         raise ValueError(f"{what}: {name}: must be a CUDA tensor of the call's device")
     sb, st, sh, sd = t.stride()
     B, T, H, _ = shape
@@ -549,18 +556,13 @@ def qk_rope_append(q, k, v, pos, inv_freq, q_out, k_pages, v_pages, block_table,
     qp, *qs = _head_rows(what, q, "q", dev, shape)
     kp, *ks = _head_rows(what, k, "k", dev, kshape)
     vp, *vs = _head_rows(what, v, "v", dev, kshape)
-    pp, fp, op, kpp, vpp, tp, lp = _ptrs(
-        what, dev, (pos, "pos", torch.int32, (B, T)), (inv_freq, "inv_freq", torch.float32, (half,)),
-        (q_out, "q_out", torch.bfloat16, shape), (k_pages, "k_pages", torch.bfloat16, pool),
-        (v_pages, "v_pages", torch.bfloat16, pool), (block_table, "block_table", torch.int32, (B, width)),
-        (prefix_len, "prefix_len", torch.int32, (B,)))
-    qn = kn = np_ = None
-    if q_norm is not None:
-        qn, = _ptrs(what, dev, (q_norm, "q_norm", torch.bfloat16, (dh,)))
-    if k_norm is not None:
-        kn, = _ptrs(what, dev, (k_norm, "k_norm", torch.bfloat16, (dh,)))
-    if n_new is not None:
-        np_, = _ptrs(what, dev, (n_new, "n_new", torch.int32, (B,)))
+    pp, fp, op, kpp, vpp, tp, lp, qn, kn, np_ = _ptrs(
+        what, dev, (pos, "pos", _I32, (B, T)), (inv_freq, "inv_freq", _F32, (half,)), (q_out, "q_out", _BF16, shape),
+        (k_pages, "k_pages", _BF16, pool), (v_pages, "v_pages", _BF16, pool),
+        (block_table, "block_table", _I32, (B, width)), (prefix_len, "prefix_len", _I32, (B,)),
+        _NONE if q_norm is None else (q_norm, "q_norm", _BF16, (dh,)),
+        _NONE if k_norm is None else (k_norm, "k_norm", _BF16, (dh,)),
+        _NONE if n_new is None else (n_new, "n_new", _I32, (B,)))
     _launch("md_qk_rope_append", lib().md_qk_rope_append, dev, stream, qp, kp, vp, _I64x9(*qs, *ks, *vs), pp, fp, 2 * half,
             1 if interleaved else 0, qn, kn, eps, op, kpp, vpp, pages, page, tp, width, lp, np_, B, T, Hq, Hkv, dh)
 
@@ -573,9 +575,9 @@ def tree_commit_paged(k_pages, v_pages, block_table, tree: Tree, prefix_len, acc
     layers, pages, Hkv, page, dh = _pool_dims(what, k_pages)
     B, width = _dims(what, block_table, "block_table", 2)
     cols = _dims(what, path, "path", 2)[1]
-    dev, i32, rows = k_pages.get_device(), torch.int32, (B,)
+    dev, i32, rows = k_pages.get_device(), _I32, (B,)
     kp, vp, tp, lp, ap, pp, bp, np_, rp, hp = _ptrs(
-        what, dev, (k_pages, "k_pages", torch.bfloat16, k_pages.shape), (v_pages, "v_pages", torch.bfloat16, k_pages.shape),
+        what, dev, (k_pages, "k_pages", _BF16, k_pages.shape), (v_pages, "v_pages", _BF16, k_pages.shape),
         (block_table, "block_table", i32, (B, width)), (prefix_len, "prefix_len", i32, rows),
         (accept_len, "accept_len", i32, rows), (path, "path", i32, (B, cols)), (bonus, "bonus", i32, rows),
         (new_prefix_len, "new_prefix_len", i32, rows), (next_root, "next_root", i32, rows),
@@ -589,9 +591,11 @@ def pages_resize(block_table, n_pages, refcount, length, page_size, extra=0, str
     [pages] in row order) or shrink to ceil((length + extra) / page_size) pages, in place.
     length [B]; -1 frees the row."""
     what = "pages_resize"
+    if not (0 < page_size < 2 ** 31 and 0 <= extra < 2 ** 31):
+        raise ValueError(f"{what}: page_size {page_size} or extra {extra} out of range")
     B, width = _dims(what, block_table, "block_table", 2)
     pages = _dims(what, refcount, "refcount", 1)[0]
-    dev, i32 = block_table.get_device(), torch.int32
+    dev, i32 = block_table.get_device(), _I32
     tp, np_, rp, lp = _ptrs(what, dev, (block_table, "block_table", i32, (B, width)), (n_pages, "n_pages", i32, (B,)),
                             (refcount, "refcount", i32, (pages,)), (length, "length", i32, (B,)))
     _launch("md_pages_resize", lib().md_pages_resize, dev, stream, tp, np_, rp, lp, B, width, pages, page_size, extra)
@@ -611,12 +615,12 @@ def pages_fork(k_pages, v_pages, block_table, n_pages, refcount, src, dst, lengt
     layers, pages, Hkv, page, dh = _pool_dims(what, k_pages)
     B, width = _dims(what, block_table, "block_table", 2)
     n = _dims(what, src, "src", 1)[0]
-    dev, i32 = k_pages.get_device(), torch.int32
+    dev, i32 = k_pages.get_device(), _I32
     kp, vp, tp, np_, rp, sp, dp, lp, wp = _ptrs(
-        what, dev, (k_pages, "k_pages", torch.bfloat16, k_pages.shape), (v_pages, "v_pages", torch.bfloat16, k_pages.shape),
+        what, dev, (k_pages, "k_pages", _BF16, k_pages.shape), (v_pages, "v_pages", _BF16, k_pages.shape),
         (block_table, "block_table", i32, (B, width)), (n_pages, "n_pages", i32, (B,)),
         (refcount, "refcount", i32, (pages,)), (src, "src", i32, (n,)), (dst, "dst", i32, (n,)),
-        (length, "length", i32, (B,)), (ws, "ws", torch.uint8, getattr(ws, "shape", ())))
+        (length, "length", i32, (B,)), (ws, "ws", _U8, getattr(ws, "shape", ())))
     _launch("md_pages_fork", lib().md_pages_fork, dev, stream, kp, vp, layers, pages, Hkv, page, dh, tp, np_, rp, lp, B,
             width, sp, dp, n, wp, ws.numel())
 

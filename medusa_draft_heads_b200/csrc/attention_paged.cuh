@@ -56,10 +56,14 @@
 // about 8 us, are as much as the walk (70B tree over 4096 slots: 23.6 us).
 #pragma once
 
+#include "attention_tc.cuh"
 #include "common.cuh"
 
 namespace md {
 namespace attn_paged {
+
+using attn_tc::exp2_sfu;
+using attn_tc::visible_bits;
 
 constexpr int kBM = 128;              // rows of a tile
 constexpr int kBN = 128;              // keys of a chunk (a slot of the rings)
@@ -124,12 +128,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-
-__device__ __forceinline__ float exp2_sfu(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // 32 columns of this thread's TMEM lane, requested only: tmem_ld_wait() and then
@@ -219,18 +217,6 @@ template <int N>
 struct IntTag {
   static constexpr int value = N;
 };
-
-// Visibility of the 64 keys n0 .. n0 + 63 (n = slot - P) as bit j: prefix keys
-// (n < 0) always, tree node n iff it is in the row's ancestor set.
-__device__ __forceinline__ uint64_t visible_bits(uint64_t lo, uint64_t hi, int n0) {
-  if (n0 <= -64) return ~0ull;
-  if (n0 >= 128) return 0ull;
-  if (n0 < 0) return (lo << (-n0)) | ((1ull << (-n0)) - 1ull);
-  if (n0 == 0) return lo;
-  if (n0 < 64) return (lo >> n0) | (hi << (64 - n0));
-  if (n0 == 64) return hi;
-  return hi >> (n0 - 64);
-}
 
 __device__ __forceinline__ bool bf16_finite(uint32_t v) { return (v & 0x7F80u) != 0x7F80u; }
 
@@ -370,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t* trow = a.table + size_t(b) * a.max_pages;
   auto v_slot = [&](int s) -> uint8_t* { return s < 2 ? sV + s * C::kTile : sQ + C::kQTile; };
 
-  if (warp < 4) {
   if (warp == 0) {
     // ------------------------------------ K ------------------------------------
     bool ok = true;
@@ -444,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = (n > vst ? n - vst : 0); c < n; ++c)
       if (c != withhold) ok = wait_phase(smem_u32(&v_full[c % vst]), (c / vst) & 1) && ok;
     if (!ok && lane == 0) set_status(MD_DEV_TIMEOUT);
-  } else {
+  } else if (warp < 4) {
     // --------------------------- MMAs: warp 1 + 2 w, stream w ---------------------------
     // The whole warp walks the stream's jobs, convergent; one elected lane issues.
     // A warp per stream: one stream's waits do not keep the other's MMAs back.
@@ -538,10 +523,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_phase(smem_u32(mma_done), 0)) ok = false;
       if (!ok && lane == 0) set_status(MD_DEV_TIMEOUT);
     }
-    }
-    __syncwarp();
-    cluster_sync();                      // the softmax warps' two barriers
-    cluster_sync();
   } else {
     // --------------------------------- softmax ---------------------------------
     const int w = (warp - 4) >> 3;                       // stream
@@ -665,16 +646,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp_live) named_bar_sync(pair_bar, 64);         // the last maxima have been read
     if (half == 1) s_part[(2 * w + 1) * kBM + r] = run_l;
     named_bar_sync(9, kSoftThreads);                     // both streams are past their last look at the ring
-    float* sO = reinterpret_cast<float*>(smem) + size_t(w) * kBM * C::kLd;
+    if (half == 0)
+      sML[w * kBM + r] = staged ? make_float2(run_m, run_l + s_part[(2 * w + 1) * kBM + r]) : make_float2(-INFINITY, 0.f);
+    // With one tile both streams' results are of the same rows: stream 0 stages its own
+    // against their common maximum, stream 1 adds to it.
+    float* sO = reinterpret_cast<float*>(smem) + (two ? size_t(w) * kBM * C::kLd : 0) + r * C::kLd;
+    float fold = 1.f;
+    float2 both = make_float2(-INFINITY, 0.f);
+    bool onto = false;                                   // stream 1: stream 0 staged this row
+    if (!two) {
+      named_bar_sync(9, kSoftThreads);
+      const float2 x = sML[r], y = sML[kBM + r];
+      const float m = fmaxf(x.x, y.x);
+      const float f0 = x.x == -INFINITY ? 0.f : exp2_sfu(x.x - m), f1 = y.x == -INFINITY ? 0.f : exp2_sfu(y.x - m);
+      both = make_float2(m, (x.x == -INFINITY ? 0.f : x.y * f0) + (y.x == -INFINITY ? 0.f : y.y * f1));
+      fold = w == 0 ? f0 : f1;
+      onto = w == 1 && x.x != -INFINITY;
+      staged = staged && __any_sync(0xffffffffu, (w == 0 ? x.x : y.x) != -INFINITY);
+      if (w == 1) named_bar_sync(9, kSoftThreads);       // stream 0's rows are staged
+    }
     if (staged && warp_live) {
       tc_fence_after();
+#pragma unroll 1
+      for (int e0 = half * (DH / 2); e0 < (half + 1) * (DH / 2); e0 += 16) {
+        float o[16];
+        tmem_ld16(tO + e0, o);
 #pragma unroll
-      for (int e0 = half * (DH / 2); e0 < (half + 1) * (DH / 2); e0 += 32) {
-        float o[32];
-        tmem_ld32(tO + e0, o);
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(sO + r * C::kLd + e0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        for (int e = 0; e < 16; e += 4) {
+          float4* to = reinterpret_cast<float4*>(sO + e0 + e);
+          float4 v = make_float4(o[e] * fold, o[e + 1] * fold, o[e + 2] * fold, o[e + 3] * fold);
+          if (onto) {
+            const float4 x = *to;
+            if (fold == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);   // nothing of this row in stream 1
+            v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+          }
+          *to = v;
+        }
       }
       if (*bad_v && live) {
         // elements of visible nodes' V that are not finite, left out of P V
@@ -686,18 +693,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (pg < 0 || pg >= a.pool) continue;
           const uint16_t* v = a.v_pages + ((size_t(pg) * a.Hkv + hk) * a.page + slot % a.page) * DH;
           for (int e = half * (DH / 2); e < (half + 1) * (DH / 2); ++e)
-            if (!bf16_finite(v[e])) sO[r * C::kLd + e] += bf16_to_f32(v[e]);
+            if (!bf16_finite(v[e])) sO[e] += bf16_to_f32(v[e]);
         }
       }
     }
-    if (half == 0)
-      sML[w * kBM + r] = staged ? make_float2(run_m, run_l + s_part[(2 * w + 1) * kBM + r]) : make_float2(-INFINITY, 0.f);
+    if (!two) {
+      if (w == 0) named_bar_sync(9, kSoftThreads);
+      else if (half == 0) sML[r] = both;                 // every thread has read the streams' own
+    }
 
     // ----------------- join the streams and splits of each row -----------------
     __syncwarp();
     cluster_sync();                      // every split's streams are staged
-    // a row's partial results: (split, stream) with one tile, (split) with two
-    const int np = two ? a.splits : 2 * a.splits;
+    const int np = a.splits;                             // a row's partial results
     const int ntok = min(two ? 2 * a.tpt : a.tpt, T - tok0);
     const int rows = ntok * a.G;                         // dense over the unit's (node, head) pairs
     const int tile_rows = a.tpt * a.G;
@@ -710,10 +718,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2* sP = sML + 2 * kBM;
     float* sW = reinterpret_cast<float*>(sP + 2 * kBM + 2 * kMaxSplits);
     const int nw = (r1 - r0) * np;
-    if (tid < nw) {                                      // at most 2 * 128 + 2 * 16 pairs
+    if (tid < nw) {                                      // at most 2 * 128 + 16 pairs
       const int i = tid / np, p = tid - i * np;
       const int w0 = (r0 + i) / tile_rows, row = r0 + i - w0 * tile_rows;   // stream (two tiles) and row in it
-      sP[tid] = ld_cluster_f2(mapa_shared(smem_u32(&sML[(two ? w0 : p & 1) * kBM + row]), uint32_t(two ? p : p >> 1)));
+      sP[tid] = ld_cluster_f2(mapa_shared(smem_u32(&sML[w0 * kBM + row]), uint32_t(p)));
     }
     named_bar_sync(9, kSoftThreads);
     if (tid < nw) {
@@ -738,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pr = r0 + i / kF4;                       // (node, head) pair of the unit
       const int w0 = pr / tile_rows, row = pr - w0 * tile_rows;
       const float* sw = sW + (i / kF4) * np;
-      const uint32_t src = smem_u32(smem) + uint32_t((row * C::kLd + (i % kF4) * 4) * 4);
+      const uint32_t src = smem_u32(smem) + uint32_t(((w0 * kBM + row) * C::kLd + (i % kF4) * 4) * 4);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
       for (int p0 = 0; p0 < np; p0 += kP) {
@@ -748,9 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < kP; ++e) {
           const int p = p0 + e;
           wgt[e] = p < np ? sw[p] : -1.f;
-          const int st = two ? w0 : p & 1, sp = two ? p : p >> 1;
           o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (!(wgt[e] < 0.f)) o[e] = ld_cluster_f4(mapa_shared(src + st * (kBM * C::kLd * 4), uint32_t(sp)));
+          if (!(wgt[e] < 0.f)) o[e] = ld_cluster_f4(mapa_shared(src, uint32_t(p)));
         }
 #pragma unroll
         for (int e = 0; e < kP; ++e) {
@@ -771,7 +778,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_sync();                      // peers are done reading this CTA's shared memory
   }
-
+  if (warp < 4) {                        // the other warps' part of the softmax warps' two cluster barriers
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -953,7 +953,7 @@ PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, i
   const int G = Hq / Hkv;
   p.tpt = md::attn_paged::kBM / G;
   p.tpu = p.splits = 1;
-  p.sort = B > 1;
+  p.sort = 0;
   const int tiles = p.units = (T + p.tpt - 1) / p.tpt;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return p;
@@ -986,7 +986,7 @@ PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, i
         p.tpu = tpu;
         p.units = units;
         p.splits = s;
-        p.sort = B > 1 && waves;
+        p.sort = B > 1 && B <= 256 && waves;   // ranking costs B^2 / 640 steps a CTA; many requests even out
       }
     }
   }
@@ -1604,7 +1604,9 @@ namespace {
 md_status paged_check(int32_t B, int32_t pool_pages, int32_t page_size, int32_t max_pages, int32_t Hkv, int32_t dh) {
   if (B < 1 || pool_pages < 1 || page_size < 1 || max_pages < 1 || Hkv < 1) return MD_ERR_INVALID_ARG;
   if (dh != 64 && dh != 128) return MD_ERR_UNSUPPORTED;
-  if (B > 65535 || int64_t(pool_pages) * Hkv > INT32_MAX || int64_t(max_pages) * page_size > INT32_MAX)
+  // slots, table entries and page rows (one page past the pool included) are int32
+  if (B > 65535 || (int64_t(pool_pages) + 1) * Hkv > INT32_MAX || int64_t(max_pages) * page_size > INT32_MAX - 256 ||
+      int64_t(B) * max_pages > INT32_MAX)
     return MD_ERR_UNSUPPORTED;
   return MD_OK;
 }
@@ -1616,7 +1618,7 @@ md_status md_attention_paged_workspace(int32_t B, int32_t T, int32_t Hq, int32_t
   if (!bytes || T < 1 || Hq < 1) return MD_ERR_INVALID_ARG;
   md_status s = paged_check(B, 1, page_size, max_pages, Hkv, dh);
   if (s != MD_OK) return s;
-  if (T > MD_MAX_T || Hq % Hkv != 0 || Hq / Hkv > 16 || page_size % 16 != 0) return MD_ERR_UNSUPPORTED;
+  if (T > MD_MAX_T || Hq % Hkv != 0 || Hq / Hkv > 16 || Hkv > 4095 || page_size % 16 != 0) return MD_ERR_UNSUPPORTED;
   *bytes = 256;
   return MD_OK;
 }
@@ -1633,7 +1635,8 @@ md_status md_tree_attention_paged(const md_bf16* q, const md_bf16* k_pages, cons
   if ((s = paged_check(B, pool_pages, page_size, max_pages, Hkv, dh)) != MD_OK) return s;
   if (!(scale >= 0.f) || !std::isfinite(scale) || (out_type != MD_OUT_F32 && out_type != MD_OUT_BF16))
     return MD_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16)) return MD_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) || out == q)
+    return MD_ERR_INVALID_ARG;
   if (!ws || ws_bytes < need || !aligned(ws, 256)) return MD_ERR_WORKSPACE;
   const PagedAttnPlan pl = paged_attn_plan(B, tree->tp.T, Hq, Hkv, dh, page_size, max_pages, out_type == MD_OUT_F32);
   md::attn_paged::Args a;

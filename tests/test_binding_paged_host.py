@@ -83,6 +83,9 @@ def test_page_calls_arguments():
         md.pages_resize(i32(B), i32(B), i32(pages), i32(B), page)
     with pytest.raises(ValueError, match="must be a CUDA tensor"):
         md.pages_resize(i32(B, width), i32(B), i32(pages), i32(B), page)
+    for bad in (dict(page_size=0), dict(page_size=2 ** 32 + 16), dict(page_size=16, extra=-1), dict(page_size=16, extra=2 ** 31)):
+        with pytest.raises(ValueError, match="out of range"):
+            md.pages_resize(i32(B, width), i32(B), i32(pages), i32(B), **bad)
     with pytest.raises(ValueError, match="k_pages: expected 4 or 5 dims"):
         md.pages_fork(bf(page, dh), bf(page, dh), i32(B, width), i32(B), i32(pages), i32(1), i32(1), i32(B),
                       torch.zeros(256, dtype=torch.uint8))
@@ -99,15 +102,17 @@ def test_c_checks_come_before_any_launch(tree):
     assert ws(1, 17, 4, 2, 64, 16, 8) == 0 and n.value > 0
     assert ws(0, 17, 4, 2, 64, 16, 8) == -1 and ws(1, 17, 4, 2, 64, 0, 8) == -1
     for bad in ((1, 129, 4, 2, 64, 16, 8), (1, 17, 5, 2, 64, 16, 8), (1, 17, 34, 2, 64, 16, 8), (1, 17, 4, 2, 96, 16, 8),
-                (1, 17, 4, 2, 64, 24, 8), (65536, 17, 4, 2, 64, 16, 8), (1, 17, 4, 2, 64, 16, 1 << 28)):
+                (1, 17, 4, 2, 64, 24, 8), (65536, 17, 4, 2, 64, 16, 8), (1, 17, 4, 2, 64, 16, 1 << 27),
+                (60000, 17, 4, 2, 64, 16, 40000), (1, 17, 4096, 4096, 64, 16, 8)):
         assert ws(*bad) == -2, bad
     p = 1 << 20
 
-    def attention(q=p, k=p, tb=p, pool=8, ps=16, w=8, scale=0.0, out=p, kind=0, wsp=p, wsn=4096):
+    def attention(q=p, k=p, tb=p, pool=8, ps=16, w=8, scale=0.0, out=p + 4096, kind=0, wsp=p, wsn=4096):
         return L.md_tree_attention_paged(q, k, p, pool, ps, tb, w, p, tree.handle, 2, 4, 2, 64, scale, out, kind, wsp, wsn, None)
 
     assert attention(q=None) == -1 and attention(tb=None) == -1 and attention(out=None) == -1
     assert attention(q=p + 2) == -1 and attention(k=p + 8) == -1 and attention(out=p + 4) == -1
+    assert attention(q=p, out=p) == -1                 # results over the queries that other CTAs still read
     assert attention(scale=-1.0) == -1 and attention(scale=float("nan")) == -1 and attention(kind=2) == -1
     assert attention(pool=0) == -1 and attention(pool=1 << 30) == -2
     assert attention(wsp=None) == -4 and attention(wsn=8) == -4 and attention(wsp=p + 16) == -4

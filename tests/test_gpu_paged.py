@@ -561,7 +561,7 @@ def test_two_streams_with_workspaces_of_their_own():
     assert all(torch.equal(o, want) for per in outs for o in per) and md.device_status() == 0
 
 
-@pytest.mark.parametrize("B,T,Hq,Hkv,page,P", [(40, 1, 8, 1, 16, (0, 700)), (70, 17, 8, 2, 32, (1, 300)), (24, 65, 8, 4, 64, (0, 400))])
+@pytest.mark.parametrize("B,T,Hq,Hkv,page,P", [(40, 1, 8, 1, 16, (0, 700)), (70, 17, 8, 2, 32, (1, 300)), (24, 65, 8, 4, 64, (0, 400)), (300, 1, 2, 1, 16, (0, 90))])
 def test_more_units_than_one_wave(B, T, Hq, Hkv, page, P):
     """Grids past one wave, requests taken from the longest down."""
     rng = np.random.default_rng(B)
