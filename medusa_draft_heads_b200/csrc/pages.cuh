@@ -45,16 +45,27 @@ __device__ __forceinline__ int block_incl_scan(int v, int* part, int& total) {
   return v + (warp > 0 ? part[warp - 1] : 0);
 }
 
-// Drops one reference to a page. A page that is not in the pool, or that
-// nobody holds, is flagged and its count stays.
-__device__ __forceinline__ void drop_page(int32_t* refcount, int pool, int page) {
-  if (page < 0 || page >= pool) {
-    set_status(MD_DEV_BAD_PAGE);
-    return;
-  }
-  if (atomicSub(&refcount[page], 1) <= 0) {
-    atomicAdd(&refcount[page], 1);
-    set_status(MD_DEV_BAD_PAGE);
+// Drops one reference each to the pages of entries[0 .. n), `lanes` lanes of a warp
+// sharing the work, four atomics of a lane in flight (their results are checked). A
+// page that is not in the pool, or that nobody holds, is flagged and its count
+// stays. The entries become -1 if `clear`.
+__device__ __forceinline__ void drop_pages(int32_t* refcount, int pool, int32_t* entries, int n, int lane, int lanes,
+                                           bool clear) {
+  for (int i0 = lane; i0 < n; i0 += 4 * lanes) {
+    int page[4], held[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) page[k] = i0 + k * lanes < n ? entries[i0 + k * lanes] : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) held[k] = page[k] >= 0 && page[k] < pool ? atomicSub(&refcount[page[k]], 1) : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i0 + k * lanes >= n) continue;
+      if (held[k] <= 0) {
+        if (page[k] >= 0 && page[k] < pool) atomicAdd(&refcount[page[k]], 1);
+        set_status(MD_DEV_BAD_PAGE);
+      }
+      if (clear) entries[i0 + k * lanes] = -1;
+    }
   }
 }
 
@@ -124,20 +135,41 @@ __global__ void __launch_bounds__(kThreads) pages_resize_kernel(ResizeArgs a) {
   __shared__ int part[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  for (int b = warp; b < a.B; b += kWarps) {     // a warp per row: give back
-    const int held = a.n_pages[b];
-    const int want = wanted_pages(a, b, held);
-    if (want < 0) {
-      if (lane == 0) set_status(held < 0 || held > a.max_pages ? MD_DEV_BAD_PAGE : MD_DEV_BAD_PREFIX);
-      continue;
+  // give back: a lane looks at a row, then the warp works through those that hold too
+  // much, long ones together, short ones four at a time
+  for (int k0 = 0; k0 * kWarps < a.B; k0 += 32) {
+    const int b = (k0 + lane) * kWarps + warp;
+    int held = 0, want = 0;
+    if (b < a.B) {
+      held = a.n_pages[b];
+      want = wanted_pages(a, b, held);
+      if (want < 0) {
+        set_status(held < 0 || held > a.max_pages ? MD_DEV_BAD_PAGE : MD_DEV_BAD_PREFIX);
+        held = want;                             // left alone
+      }
     }
-    int32_t* row = a.table + size_t(b) * a.max_pages;
-    for (int i = want + lane; i < held; i += 32) {
-      drop_page(a.refcount, a.pool, row[i]);
-      row[i] = -1;
+    uint32_t shrinks = __ballot_sync(0xffffffffu, held > want);
+    const uint32_t longs = __ballot_sync(0xffffffffu, held - want > 32);
+    for (uint32_t m = longs; m != 0; m &= m - 1) {
+      const int i = __ffs(m) - 1;
+      const int rw = __shfl_sync(0xffffffffu, want, i), rh = __shfl_sync(0xffffffffu, held, i);
+      const int rb = __shfl_sync(0xffffffffu, b, i);
+      drop_pages(a.refcount, a.pool, a.table + size_t(rb) * a.max_pages + rw, rh - rw, lane, 32, true);
     }
-    __syncwarp();
-    if (lane == 0 && held > want) a.n_pages[b] = want;
+    for (uint32_t m = shrinks & ~longs; m != 0;) {
+      uint32_t mine = 0;                         // this quarter of the warp's row, as a bit
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t low = m & (0u - m);
+        if (k == lane >> 3) mine = low;
+        m ^= low;
+      }
+      const int i = mine ? __ffs(mine) - 1 : 0;
+      const int rw = __shfl_sync(0xffffffffu, want, i), rh = __shfl_sync(0xffffffffu, held, i);
+      const int rb = __shfl_sync(0xffffffffu, b, i);
+      if (mine) drop_pages(a.refcount, a.pool, a.table + size_t(rb) * a.max_pages + rw, rh - rw, lane & 7, 8, true);
+    }
+    if (held > want) a.n_pages[b] = want;
   }
   __syncthreads();
 
@@ -254,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(ForkArgs a) {
   for (int f = warp; f < a.n; f += kWarps) {
     if (s_src[f] < 0) continue;
     const int d = s_dst[f], held = a.n_pages[d];
-    for (int p = lane; p < held; p += 32) drop_page(a.refcount, a.pool, a.table[size_t(d) * a.max_pages + p]);
+    drop_pages(a.refcount, a.pool, a.table + size_t(d) * a.max_pages, held, lane, 32, false);
   }
   __syncthreads();
   // a new page for every fork that ends inside one, lowest ids in list order
