@@ -7,7 +7,8 @@
 // block_table[b, s / page]. The T * G query rows (node, head of the group) of a
 // KV head share its keys, so scores and weighted sums are dense products.
 //
-// CTA = (KV split, unit of one or two 128-row tiles, KV head, request). Two streams,
+// CTA = (KV split, unit of one or two 128-row tiles, KV head, request). Two streams
+// (one, with half of everything, where there are many short requests: Cfg),
 // each with scores S, weights P (written over S) and an accumulator O in TMEM, walk
 // the split's keys in jobs of 64:
 //   - two tiles: stream w is row tile w and takes every job, so that a chunk of
@@ -53,7 +54,8 @@
 // without the softmax: S with N = 64 is held back by shared memory, 43 clocks an MMA
 // against 32) and the special-function unit 1.08; 70B batch of 8: 103 us, 0.66
 // PFLOP/s. One request: set-up, first loads, the splits' joining and the launch,
-// about 8 us, are as much as the walk (70B tree over 4096 slots: 23.6 us).
+// about 8 us, are as much as the walk (70B tree over 4096 slots: 22.5 us). Many
+// requests of few keys: the same fixed part once a CTA, halved by two CTAs an SM.
 #pragma once
 
 #include "attention_tc.cuh"
@@ -66,18 +68,22 @@ using attn_tc::exp2_sfu;
 using attn_tc::visible_bits;
 
 constexpr int kBM = 128;              // rows of a tile
-constexpr int kBN = 128;              // keys of a chunk (a slot of the rings)
 constexpr int kSub = 64;              // keys of a job: half a chunk
-constexpr int kThreads = 640;
-constexpr int kSoftThreads = 512;
-constexpr int kKStages = 3;
-constexpr int kVStages = 3;           // the third only with one row tile
+constexpr int kMaxStages = 3;
 constexpr int kMaxSplits = 16;        // CTAs of a cluster (above 8 by opt-in)
 constexpr float kRescaleLog2 = 8.0f;
-constexpr uint32_t kTmemCols = 512;   // S0, S1, O0, O1: 128 columns each
 
-template <int DH, bool F32>
+// STREAMS = 2: one CTA per SM, as above. STREAMS = 1: half a CTA of everything (one
+// stream, one row tile, chunks of 64 keys), two to an SM, so that one's set-up and
+// read-out run beside the other's walk: for grids of many short requests (256 of 200
+// slots, 8 KV heads, one node: 189 us with two streams, 105 with one).
+template <int DH, bool F32, int STREAMS>
 struct Cfg {
+  static constexpr int kBN = 64 * STREAMS;                 // keys of a chunk (a slot of the rings)
+  static constexpr int kSoftThreads = 256 * STREAMS;
+  static constexpr int kThreads = 128 + kSoftThreads;
+  static constexpr int kKStages = STREAMS == 2 ? 3 : 2;
+  static constexpr uint32_t kTmemCols = 256 * STREAMS;     // S and O of each stream: 128 columns each
   // bf16 results: two S buffers a stream, so that the next scores are ready when a
   // job ends; fp32 ones: the three parts of P take the columns of the second
   static constexpr int kBufs = F32 ? 1 : 2;
@@ -86,10 +92,11 @@ struct Cfg {
   static constexpr uint32_t kQTile = KB * kBM * 128;       // 128 rows x DH bf16, 128-byte swizzle
   static constexpr uint32_t kTile = KB * kBN * 128;        // a chunk of K or V
   static constexpr int kLd = DH + 4;                       // padded fp32 row of the staged O
-  // Q0, Q1 (or a V slot), 3 K slots, 2 V slots
-  static constexpr uint32_t kRing = 2 * kQTile + 5 * kTile;
-  static constexpr int kSmem = int(kRing) + 512 + 2048;    // + barriers, row maxima
-  static_assert(2 * kBM * (kLd * 4 + 8) + (2 * kBM + 2 * kMaxSplits) * 12 <= int(kRing), "staged O, (m, sum), weights");
+  // a Q tile per stream (the second may be a V slot), the K slots, 2 V slots
+  static constexpr uint32_t kRing = STREAMS * kQTile + (kKStages + 2) * kTile;
+  static constexpr int kSmem = int(kRing) + 512 + 1024 * STREAMS;   // + barriers, row maxima
+  static_assert(STREAMS * kBM * (kLd * 4 + 8) + (STREAMS * kBM + 2 * kMaxSplits) * 12 <= int(kRing),
+                "staged O, (m, sum), weights");
 };
 
 struct Args {
@@ -98,7 +105,7 @@ struct Args {
   const int32_t* prefix_len;   // [B]
   void* out;                   // [B, T, Hq, dh]
   int B, Hq, Hkv, G, pool, page, max_pages;
-  int piece;                   // rows of a TMA copy: the largest power of two dividing page, at most 128
+  int piece;                   // rows of a TMA copy: the largest power of two dividing page, within a chunk
   int tpt;                     // tree nodes of a row tile
   int tpu;                     // row tiles of a unit: 1 or 2
   int units, splits, sort;
@@ -213,6 +220,11 @@ __device__ __forceinline__ uint32_t high_halves(float a, float b) {
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 
+template <int ID, int THREADS>
+__device__ __forceinline__ void fixed_bar_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+
 template <int N>
 struct IntTag {
   static constexpr int value = N;
@@ -225,10 +237,11 @@ __device__ __forceinline__ bool bf16_finite(uint32_t v) { return (v & 0x7F80u) !
 struct Piece {
   int page, at;
 };
+template <int BN>
 __device__ __forceinline__ Piece piece_of(const int32_t* row, int key0, int nkeys, const Args& a) {
   const int key = key0 + int(threadIdx.x & 31) * a.piece;
   Piece p = {0, 0};
-  if (key < min(nkeys, key0 + kBN)) {
+  if (key < min(nkeys, key0 + BN)) {
     const int pi = key / a.page;
     p.page = row[pi];
     p.at = key - pi * a.page;
@@ -238,10 +251,11 @@ __device__ __forceinline__ Piece piece_of(const int32_t* row, int key0, int nkey
 
 // The copies of one chunk of K or V into a ring slot, each lane a page piece.
 // Pieces behind the last slot are not copied. All lanes of a warp call it.
-template <int DH, bool F32>
+template <int DH, bool F32, int STREAMS>
 __device__ __forceinline__ void load_chunk(uint32_t dst, const CUtensorMap* map, uint32_t bar, Piece p, int key0, int nkeys,
                                            int hk, const Args& a) {
-  using C = Cfg<DH, F32>;
+  using C = Cfg<DH, F32, STREAMS>;
+  constexpr int kBN = C::kBN;
   const int lane = threadIdx.x & 31;
   const int pieces = (min(kBN, nkeys - key0) + a.piece - 1) / a.piece;
   if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(pieces * a.piece) * DH * 2);
@@ -257,23 +271,26 @@ __device__ __forceinline__ void load_chunk(uint32_t dst, const CUtensorMap* map,
   }
 }
 
-template <int DH, bool F32>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int DH, bool F32, int STREAMS>
+__global__ void __launch_bounds__(Cfg<DH, F32, STREAMS>::kThreads, 3 - STREAMS)
     attn_paged_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeParams tp, Args a) {
-  using C = Cfg<DH, F32>;
+  using C = Cfg<DH, F32, STREAMS>;
+  constexpr int kBN = C::kBN, kKStages = C::kKStages;
+  constexpr bool kPair = STREAMS == 2;
+  constexpr int kAllBar = 1 + 4 * STREAMS;               // named barrier of the softmax warps, behind those of pairs
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* sQ = smem;                                    // 2 tiles (the second may be V slot 2)
-  uint8_t* sK = smem + 2 * C::kQTile;                    // 3 slots
+  uint8_t* sQ = smem;                                    // a tile per stream (the second may be V slot 2)
+  uint8_t* sK = smem + STREAMS * C::kQTile;              // the K slots
   uint8_t* sV = sK + kKStages * C::kTile;                // 2 slots
-  float2* sML = reinterpret_cast<float2*>(smem + 2 * kBM * C::kLd * 4);   // [2][128], behind the staged O
+  float2* sML = reinterpret_cast<float2*>(smem + STREAMS * kBM * C::kLd * 4);   // [streams][128], behind the staged O
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing);
   uint64_t* q_full = bars;                // 1
-  uint64_t* k_full = q_full + 1;          // 3
-  uint64_t* k_empty = k_full + kKStages;  // 3
-  uint64_t* v_full = k_empty + kKStages;  // 3
-  uint64_t* v_empty = v_full + kVStages;  // 3
-  uint64_t* s_full = v_empty + kVStages;  // [2 streams][2 buffers]
+  uint64_t* k_full = q_full + 1;          // up to 3
+  uint64_t* k_empty = k_full + kMaxStages;
+  uint64_t* v_full = k_empty + kMaxStages;
+  uint64_t* v_empty = v_full + kMaxStages;
+  uint64_t* s_full = v_empty + kMaxStages;  // [streams][2 buffers]
   uint64_t* p_full = s_full + 4;          // [2][2]
   uint64_t* o_full = p_full + 4;          // [2]
   uint64_t* v_fixed = o_full + 2;         // [2]: the chunks that reach the tree, behind the V warp's look
@@ -288,13 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int T = tp.T;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(q_full), 1);
-    for (int i = 0; i < kKStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(smem_u32(&k_full[i]), 1);
-      mbar_init(smem_u32(&k_empty[i]), 2);               // both streams
-    }
-    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(smem_u32(&k_empty[i]), STREAMS);         // every stream has used it
       mbar_init(smem_u32(&v_full[i]), 1);
-      mbar_init(smem_u32(&v_empty[i]), 2);
+      mbar_init(smem_u32(&v_empty[i]), STREAMS);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
@@ -304,13 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&o_full[i]), 1);
       mbar_init(smem_u32(&v_fixed[i]), 1);
     }
-    mbar_init(smem_u32(mma_done), 2);
+    mbar_init(smem_u32(mma_done), STREAMS);
     fence_barrier_init();
     *req = blockIdx.z;
     *bad_v = 0;
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
   if (lane == 0) {
@@ -326,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // More CTAs than one wave: requests from the longest prefix down, so that
   // short ones fill the tail.
   if (a.sort) {
-    for (int c = threadIdx.x; c < a.B; c += kThreads) {
+    for (int c = threadIdx.x; c < a.B; c += C::kThreads) {
       const int pc = a.prefix_len[c];
       int rank = 0;
       for (int j = 0; j < a.B; ++j) {
@@ -344,14 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (bad && P != -1 && split == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(MD_DEV_BAD_PREFIX);
   const int nkeys = bad ? 0 : P + T;
   const int nch_all = (nkeys + kBN - 1) / kBN;
-  // at most 2^24 chunks and 16 splits
+  // at most 2^25 chunks and 16 splits
   const int c_begin = int(uint32_t(nch_all) * uint32_t(split) / uint32_t(a.splits));
   const int nch = int(uint32_t(nch_all) * uint32_t(split + 1) / uint32_t(a.splits)) - c_begin;
   // jobs' keys: halves of chunks, without a last half that is all behind the keys
   const int nsub = nch == 0 ? 0 : (min(nkeys, (c_begin + nch) * kBN) - c_begin * kBN + kSub - 1) / kSub;
   const int tok0 = unit * a.tpu * a.tpt;               // nodes of this unit
-  const bool two = a.tpu == 2 && T - tok0 > a.tpt;     // two row tiles
-  const int vst = two ? 2 : 3;                         // V slots in use
+  const bool two = kPair && a.tpu == 2 && T - tok0 > a.tpt;   // two row tiles
+  const int vst = !kPair || two ? 2 : 3;               // V slots in use
   const int c_tree = max(0, (P - c_begin * kBN) / kBN);   // first chunk with tree slots (at most two have any), if below nch
   const int32_t* trow = a.table + size_t(b) * a.max_pages;
   auto v_slot = [&](int s) -> uint8_t* { return s < 2 ? sV + s * C::kTile : sQ + C::kQTile; };
@@ -361,17 +376,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const int withhold = *const_cast<volatile int*>(&g_withhold_chunk);   // test hook, normally -1
     int n = 0;
-    Piece next = piece_of(trow, c_begin * kBN, nch > 0 ? nkeys : 0, a);
+    Piece next = piece_of<kBN>(trow, c_begin * kBN, nch > 0 ? nkeys : 0, a);
     for (int c = 0; c < nch; ++c) {
       const int key0 = (c_begin + c) * kBN;
       const Piece p = next;
-      if (c + 1 < nch) next = piece_of(trow, key0 + kBN, nkeys, a);
+      if (c + 1 < nch) next = piece_of<kBN>(trow, key0 + kBN, nkeys, a);
       if (c == withhold) continue;
       const int st = c % kKStages;
       if (c >= kKStages && !wait_phase(smem_u32(&k_empty[st]), ((c / kKStages) - 1) & 1)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      load_chunk<DH, F32>(smem_u32(sK + st * C::kTile), &kmap, smem_u32(&k_full[st]), p, key0, nkeys, hk, a);
+      load_chunk<DH, F32, STREAMS>(smem_u32(sK + st * C::kTile), &kmap, smem_u32(&k_full[st]), p, key0, nkeys, hk, a);
       n = c + 1;
     }
     // every copy issued into this CTA's shared memory lands before it may exit
@@ -383,17 +398,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const int withhold = *const_cast<volatile int*>(&g_withhold_chunk);
     int n = 0;
-    Piece next = piece_of(trow, c_begin * kBN, nch > 0 ? nkeys : 0, a);
+    Piece next = piece_of<kBN>(trow, c_begin * kBN, nch > 0 ? nkeys : 0, a);
     for (int c = 0; c < nch; ++c) {
       const int key0 = (c_begin + c) * kBN;
       const Piece p = next;
-      if (c + 1 < nch) next = piece_of(trow, key0 + kBN, nkeys, a);
+      if (c + 1 < nch) next = piece_of<kBN>(trow, key0 + kBN, nkeys, a);
       if (c == withhold) continue;
       const int st = c % vst;
       if (c >= vst && !wait_phase(smem_u32(&v_empty[st]), ((c / vst) - 1) & 1)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      load_chunk<DH, F32>(smem_u32(v_slot(st)), &vmap, smem_u32(&v_full[st]), p, key0, nkeys, hk, a);
+      load_chunk<DH, F32, STREAMS>(smem_u32(v_slot(st)), &vmap, smem_u32(&v_full[st]), p, key0, nkeys, hk, a);
       n = c + 1;
     }
     // V rows that P's zeros must not meet: slots behind the last key, and what is
@@ -433,14 +448,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------- MMAs: warp 1 + 2 w, stream w ---------------------------
     // The whole warp walks the stream's jobs, convergent; one elected lane issues.
     // A warp per stream: one stream's waits do not keep the other's MMAs back.
-    if (nch > 0) {
+    if (nch > 0 && (warp >> 1) < STREAMS) {
       constexpr uint32_t idesc_s = umma_idesc_bf16(kBM, kSub, 0, 0);
       constexpr uint32_t idesc_o = umma_idesc_bf16(kBM, DH, 0, 1);
-      const int w = warp >> 1;
-      const uint32_t tS = __reduce_max_sync(0xffffffffu, tmem) + w * 128, tO = tS + 256;
+      const int w = kPair ? warp >> 1 : 0;
+      const uint32_t tS = __reduce_max_sync(0xffffffffu, tmem) + w * 128, tO = tS + STREAMS * 128;
       const int n = __reduce_max_sync(0xffffffffu, nsub), ct = __reduce_max_sync(0xffffffffu, c_tree);
       const uint32_t q_desc = smem_u32(sQ), k_desc = smem_u32(sK), v_desc = smem_u32(sV);
-      if (w == 1 && lane == 0) {                         // the Q tiles
+      if (w == STREAMS - 1 && lane == 0) {               // the Q tiles
         const uint32_t qb = smem_u32(q_full);
         const int tiles = two ? 2 : 1;
         mbar_arrive_expect_tx(qb, uint32_t(tiles * a.tpt * a.G) * DH * 2);
@@ -455,10 +470,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // same half of the next chunk, the other stream having taken the other (1)
       auto walk = [&](auto tiles_tag) {
         constexpr int TILES = decltype(tiles_tag)::value;
-        constexpr int VST = TILES == 2 ? 2 : 3;
-        const int jobs = TILES == 2 ? n : (n - w + 1) / 2;
+        constexpr int VST = TILES == 2 || !kPair ? 2 : 3;
+        const int jobs = TILES == 2 || !kPair ? n : (n - w + 1) / 2;
         int ks = 0, kph = 0, vs = 0, vph = 0;            // slot and phase of the next job's K and V
-        auto half_of = [&](int j) { return TILES == 2 ? j & 1 : w; };
+        auto half_of = [&](int j) { return TILES == 2 ? j & 1 : w; };      // of the job's chunk
         auto issue_s = [&](int j, int buf) {
           const int half = half_of(j);
           if (TILES == 1 || half == 0) {                 // a chunk this stream has not used yet
@@ -515,8 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j0 + i < jobs && ok) job(j0 + i, i, ph);
       };
       if (ok) {
-        if (two) walk(IntTag<2>{});
-        else walk(IntTag<1>{});
+        if constexpr (kPair) {
+          if (two) walk(IntTag<2>{});
+          else walk(IntTag<1>{});
+        } else {
+          walk(IntTag<1>{});
+        }
       }
       // every MMA issued so far completes before TMEM is read out or released
       umma_commit_elect(smem_u32(mma_done));
@@ -525,26 +544,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // --------------------------------- softmax ---------------------------------
-    const int w = (warp - 4) >> 3;                       // stream
+    const int w = kPair ? (warp - 4) >> 3 : 0;           // stream
     const int half = ((warp - 4) >> 2) & 1;              // of a job's keys, and of O's columns
     const int q = warp & 3;                              // TMEM lane quarter
-    const int pair_bar = 1 + w * 4 + q;                  // named barrier of the two halves' warps
+    // The two halves' warps. Two CTAs to an SM: ids known to the compiler, as an id in a
+    // register reserves all 16 barriers of a CTA, which then has the SM to itself.
+    auto pair_sync = [&] {
+      if constexpr (kPair) {
+        named_bar_sync(1 + w * 4 + q, 64);
+      } else {
+        switch (q) {
+          case 0: fixed_bar_sync<1, 64>(); break;
+          case 1: fixed_bar_sync<2, 64>(); break;
+          case 2: fixed_bar_sync<3, 64>(); break;
+          default: fixed_bar_sync<4, 64>();
+        }
+      }
+    };
     const int r = q * 32 + lane;                         // row of the tile
     const int tile_tok = tok0 + (two ? w * a.tpt : 0);
     const int t = tile_tok + r / a.G;
     const bool live = r < a.tpt * a.G && t < T;
     const bool warp_live = __any_sync(0xffffffffu, live);
     const uint32_t lane_off = uint32_t(q * 32) << 16;
-    const uint32_t tS = tmem + lane_off + uint32_t(w * 128), tO = tmem + lane_off + uint32_t(256 + w * 128);
+    const uint32_t tS = tmem + lane_off + uint32_t(w * 128), tO = tmem + lane_off + uint32_t((STREAMS + w) * 128);
     const int tt = live ? t : 0;
     const uint64_t anc_lo = (uint64_t(tp.anc[tt][1]) << 32) | tp.anc[tt][0];
     const uint64_t anc_hi = (uint64_t(tp.anc[tt][3]) << 32) | tp.anc[tt][2];
     const float sc = a.scale_log2;
-    const int my_jobs = two ? nsub : (nsub - w + 1) / 2;
+    const int my_jobs = two || !kPair ? nsub : (nsub - w + 1) / 2;
     float run_m = -INFINITY, run_l = 0.f;
     bool ok = true;
     for (int j = 0; j < my_jobs; ++j) {
-      const int u = two ? j : 2 * j + w;                 // half-chunk
+      const int u = two || !kPair ? j : 2 * j + w;       // 64 keys of the range
       const int buf = j % C::kBufs;
       // A wait that gives up only skips work: every iteration runs the halves' barriers.
       ok = __all_sync(0xffffffffu, ok && wait_phase(smem_u32(&s_full[2 * w + buf]), (j / C::kBufs) & 1));
@@ -573,9 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mx = max3(max3(m4[0], m4[1], m4[2]), m4[3], m4[3]);
         // the row's maximum over both halves; behind the second barrier both have
         // read their scores, and either may write P over them
-        named_bar_sync(pair_bar, 64);                    // the last job's maxima have been read
+        pair_sync();                                     // the last job's maxima have been read
         s_part[(2 * w + half) * kBM + r] = mx;
-        named_bar_sync(pair_bar, 64);
+        pair_sync();
         const float mo = s_part[(2 * w + (half ^ 1)) * kBM + r];
         mx = max3(mx, mo, mo);
         // a score that is NaN or infinite makes the row NaN, as its softmax is
@@ -643,9 +675,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool staged = ok && my_jobs > 0;
     if (nch > 0) staged = __all_sync(0xffffffffu, wait_phase(smem_u32(mma_done), 0)) && staged;
     if (c_tree < nch) staged = __all_sync(0xffffffffu, wait_phase(smem_u32(&v_fixed[nch - 1 - c_tree]), 0)) && staged;   // *bad_v
-    if (warp_live) named_bar_sync(pair_bar, 64);         // the last maxima have been read
+    if (warp_live) pair_sync();                          // the last maxima have been read
     if (half == 1) s_part[(2 * w + 1) * kBM + r] = run_l;
-    named_bar_sync(9, kSoftThreads);                     // both streams are past their last look at the ring
+    fixed_bar_sync<kAllBar, C::kSoftThreads>();          // both streams are past their last look at the ring
     if (half == 0)
       sML[w * kBM + r] = staged ? make_float2(run_m, run_l + s_part[(2 * w + 1) * kBM + r]) : make_float2(-INFINITY, 0.f);
     // With one tile both streams' results are of the same rows: stream 0 stages its own
@@ -654,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float fold = 1.f;
     float2 both = make_float2(-INFINITY, 0.f);
     bool onto = false;                                   // stream 1: stream 0 staged this row
-    if (!two) {
-      named_bar_sync(9, kSoftThreads);
+    if (kPair && !two) {
+      fixed_bar_sync<kAllBar, C::kSoftThreads>();
       const float2 x = sML[r], y = sML[kBM + r];
       const float m = fmaxf(x.x, y.x);
       const float f0 = x.x == -INFINITY ? 0.f : exp2_sfu(x.x - m), f1 = y.x == -INFINITY ? 0.f : exp2_sfu(y.x - m);
@@ -663,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fold = w == 0 ? f0 : f1;
       onto = w == 1 && x.x != -INFINITY;
       staged = staged && __any_sync(0xffffffffu, (w == 0 ? x.x : y.x) != -INFINITY);
-      if (w == 1) named_bar_sync(9, kSoftThreads);       // stream 0's rows are staged
+      if (w == 1) fixed_bar_sync<kAllBar, C::kSoftThreads>(); // stream 0's rows are staged
     }
     if (staged && warp_live) {
       tc_fence_after();
@@ -688,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < T; ++n) {
           if (!((tp.anc[t][n >> 5] >> (n & 31)) & 1u)) continue;
           const int slot = P + n, u = (slot - c_begin * kBN) / kSub;
-          if (slot < c_begin * kBN || u >= nsub || (!two && (u & 1) != w)) continue;
+          if (slot < c_begin * kBN || u >= nsub || (kPair && !two && (u & 1) != w)) continue;
           const int pg = trow[slot / a.page];
           if (pg < 0 || pg >= a.pool) continue;
           const uint16_t* v = a.v_pages + ((size_t(pg) * a.Hkv + hk) * a.page + slot % a.page) * DH;
@@ -697,8 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!two) {
-      if (w == 0) named_bar_sync(9, kSoftThreads);
+    if (kPair && !two) {
+      if (w == 0) fixed_bar_sync<kAllBar, C::kSoftThreads>();
       else if (half == 0) sML[r] = both;                 // every thread has read the streams' own
     }
 
@@ -711,19 +743,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile_rows = a.tpt * a.G;
     const int crank = int(cluster_ctarank());
     const int r0 = rows * crank / a.splits, r1 = rows * (crank + 1) / a.splits;
-    const int tid = threadIdx.x - (kThreads - kSoftThreads);
+    const int tid = threadIdx.x - (C::kThreads - C::kSoftThreads);
     // This code runs once a CTA, so what it costs is fetching it: loops stay rolled.
     // Weights of the partial results first: sW[row][p] = 2^(m_p - m) / L, or -1 where
     // nothing was staged; from (m, sum) of every partial, copied to sP[row][p].
-    float2* sP = sML + 2 * kBM;
-    float* sW = reinterpret_cast<float*>(sP + 2 * kBM + 2 * kMaxSplits);
+    float2* sP = sML + STREAMS * kBM;
+    float* sW = reinterpret_cast<float*>(sP + STREAMS * kBM + 2 * kMaxSplits);
     const int nw = (r1 - r0) * np;
     if (tid < nw) {                                      // at most 2 * 128 + 16 pairs
       const int i = tid / np, p = tid - i * np;
       const int w0 = (r0 + i) / tile_rows, row = r0 + i - w0 * tile_rows;   // stream (two tiles) and row in it
       sP[tid] = ld_cluster_f2(mapa_shared(smem_u32(&sML[w0 * kBM + row]), uint32_t(p)));
     }
-    named_bar_sync(9, kSoftThreads);
+    fixed_bar_sync<kAllBar, C::kSoftThreads>();
     if (tid < nw) {
       const int i = tid / np;
       float mx = -INFINITY, L = 0.f;
@@ -737,12 +769,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float m = sP[tid].x;
       sW[tid] = m == -INFINITY ? -1.f : exp2_sfu(m - mx) / L;
     }
-    named_bar_sync(9, kSoftThreads);
+    fixed_bar_sync<kAllBar, C::kSoftThreads>();
     // rows as float4 columns, up to kP of a thread's loads from the cluster in flight
     constexpr int kF4 = DH / 4, kP = 8;
     const int items = (r1 - r0) * kF4;
 #pragma unroll 1
-    for (int i = tid; i < items; i += kSoftThreads) {
+    for (int i = tid; i < items; i += C::kSoftThreads) {
       const int pr = r0 + i / kF4;                       // (node, head) pair of the unit
       const int w0 = pr / tile_rows, row = pr - w0 * tile_rows;
       const float* sw = sW + (i / kF4) * np;
@@ -787,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 

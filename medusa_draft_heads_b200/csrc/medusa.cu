@@ -875,12 +875,12 @@ md_status launch_attn_tc(const AttnPlan& pl, const md_bf16* q, const md_bf16* kc
 
 // ------------------------ paged attention planning -------------------------
 
-template <int DH, bool F32>
+template <int DH, bool F32, int STREAMS>
 void paged_attn_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, dim3 grid, cudaStream_t st) {
   *cfg = {};
   cfg->gridDim = grid;
-  cfg->blockDim = dim3(md::attn_paged::kThreads);
-  cfg->dynamicSmemBytes = md::attn_paged::Cfg<DH, F32>::kSmem;
+  cfg->blockDim = dim3(md::attn_paged::Cfg<DH, F32, STREAMS>::kThreads);
+  cfg->dynamicSmemBytes = md::attn_paged::Cfg<DH, F32, STREAMS>::kSmem;
   cfg->stream = st;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = grid.x;
@@ -894,22 +894,22 @@ void paged_attn_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, dim3 
 
 // Function attributes last for the process: set once per device (a call of
 // cudaFuncSetAttribute costs about a microsecond).
-template <int DH, bool F32>
+template <int DH, bool F32, int STREAMS>
 md_status paged_attn_attributes() {
   static std::atomic<bool> done[kMaxDevices];
   int dev = 0;
   md_status s = cuda_ok(cudaGetDevice(&dev));
   if (s != MD_OK) return s;
   if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return MD_OK;
-  auto kern = md::attn_paged::attn_paged_kernel<DH, F32>;
-  if ((s = set_smem(kern, md::attn_paged::Cfg<DH, F32>::kSmem)) != MD_OK) return s;
+  auto kern = md::attn_paged::attn_paged_kernel<DH, F32, STREAMS>;
+  if ((s = set_smem(kern, md::attn_paged::Cfg<DH, F32, STREAMS>::kSmem)) != MD_OK) return s;
   if ((s = cuda_ok(cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1))) != MD_OK) return s;
   if (dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
   return MD_OK;
 }
 
 // CTAs resident at once in clusters of `splits` on the current device, dev.
-template <int DH, bool F32>
+template <int DH, bool F32, int STREAMS>
 int paged_attn_slots(int dev, int splits) {
   static std::atomic<int> cache[kMaxDevices][md::attn_paged::kMaxSplits + 1];
   int n = cache[dev][splits].load(std::memory_order_relaxed);
@@ -917,10 +917,10 @@ int paged_attn_slots(int dev, int splits) {
     int clusters = 0;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    paged_attn_config<DH, F32>(&cfg, attr, dim3(splits, 64), nullptr);
+    paged_attn_config<DH, F32, STREAMS>(&cfg, attr, dim3(splits, 64), nullptr);
     cfg.numAttrs = 1;
-    if (paged_attn_attributes<DH, F32>() != MD_OK ||
-        cudaOccupancyMaxActiveClusters(&clusters, md::attn_paged::attn_paged_kernel<DH, F32>, &cfg) != cudaSuccess) {
+    if (paged_attn_attributes<DH, F32, STREAMS>() != MD_OK ||
+        cudaOccupancyMaxActiveClusters(&clusters, md::attn_paged::attn_paged_kernel<DH, F32, STREAMS>, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
       clusters = 0;
     }
@@ -931,14 +931,15 @@ int paged_attn_slots(int dev, int splits) {
 }
 
 struct PagedAttnPlan {
-  int tpt, tpu, units, splits, sort;
+  int tpt, tpu, units, splits, sort, streams;
 };
 
 // Row tiles hold whole nodes (G rows each); a unit is one or two tiles, and its
 // KV range is cut into splits. The shape with the least estimated time (us) is
 // taken, from measured costs: a CTA's fixed part (launch, first loads, read-out)
-// 8 and 10 for one and two tiles, 0.5 and 1.5 more to join splits; a chunk 0.8 for
-// one tile, 1.1 if other tiles' CTAs read the same keys from L2, 1.75 for two, twice
+// 8 and 10 for one and two tiles, 0.5 and 1.5 more to join splits; a chunk of 128 keys
+// 0.8 for one tile, 1.1 if other tiles' CTAs read the same keys from L2, 1.75 for two,
+// 1.9 for one tile and one stream beside another such CTA, twice
 // that for fp32 results (one score buffer, three P V products); CTAs
 // past one wave fill the SMs as they come, with half a CTA's time left uneven; and
 // no call is faster than its keys' bytes from memory, 1.1 times that in one wave (a
@@ -948,33 +949,49 @@ struct PagedAttnPlan {
 //     splits 26.7. B = 8: one tile 124, two tiles 113.6.
 //   Decoding, 8 KV heads, 4096 slots: 1 split 32.9, 4 15.3, 8 12.5, 12 (two waves)
 //     22.6. 16 requests of 26000: 1 split 261, 2 276; of 20001 to 32768: 316, 270.
+//   One stream against two, 32/8 heads, one node: 256 requests of 200 slots 105 against
+//     189, of 2000 365 against 446; 64 of 200 20.7 against 41.7; 32 of 500 13.2 against
+//     24.9; 64 of 17 nodes over 200 33.9 against 53.3, fp32 47.1 against 63.6.
 PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, int max_pages, bool f32) {
   PagedAttnPlan p;
   const int G = Hq / Hkv;
   p.tpt = md::attn_paged::kBM / G;
   p.tpu = p.splits = 1;
   p.sort = 0;
+  p.streams = 2;
   const int tiles = p.units = (T + p.tpt - 1) / p.tpt;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return p;
-  const int chunks = int((int64_t(max_pages) * page + md::attn_paged::kBN - 1) / md::attn_paged::kBN);
-  const double bytes_us = 4.0 * B * Hkv * dh * md::attn_paged::kBN * chunks / 6.5e6;
+  const int chunks = int((int64_t(max_pages) * page + 127) / 128);
+  const double bytes_us = 4.0 * B * Hkv * dh * 128 * chunks / 6.5e6;
+  auto slots_of = [&](int streams, int s) -> int {
+    if (streams == 1) return 2 * num_sms();   // the occupancy calculator counts a kernel with TMEM as one an SM
+    return dh == 128 ? (f32 ? paged_attn_slots<128, true, 2>(dev, s) : paged_attn_slots<128, false, 2>(dev, s))
+                     : (f32 ? paged_attn_slots<64, true, 2>(dev, s) : paged_attn_slots<64, false, 2>(dev, s));
+  };
   double best = 0;
-  for (int tpu = 1; tpu <= 2 && tpu <= tiles; ++tpu) {
+  // Shape 0: one stream a CTA, two CTAs an SM, for one row tile (with more, two tiles a
+  // CTA are as fast: 16 requests of 300 slots, two tiles, 25.2 us against 24.1). T <= 64,
+  // as its look at the tree's V spans two chunks of 64 keys. No splits: where two share
+  // an SM, a CTA that holds TMEM must not wait for its cluster's others, which may be
+  // waiting for TMEM that another kernel's CTA holds. Shapes 1 and 2: two streams, one
+  // or two tiles.
+  for (int shape = tiles == 1 && T <= 64 ? 0 : 1; shape <= 2 && shape <= tiles; ++shape) {
+    const int tpu = std::max(shape, 1), streams = shape == 0 ? 1 : 2;
     const int units = (tiles + tpu - 1) / tpu;
     const int64_t base = int64_t(B) * Hkv * units;
     // An accumulator of the tensor cores drops what it cannot hold at every step, which
     // over thousands of keys shows in fp32 results (8e-6 at 20000 keys of a stream, 7e-7 at
     // 1024): those are summed in stretches of at most 1024 keys a stream, as far as 16
     // splits reach.
-    const int least = f32 ? std::min(md::attn_paged::kMaxSplits, (chunks + 16 / tpu - 1) / (16 / tpu)) : 1;
-    for (int s = least; s <= md::attn_paged::kMaxSplits && s <= chunks; ++s) {
-      const int slots = dh == 128 ? (f32 ? paged_attn_slots<128, true>(dev, s) : paged_attn_slots<128, false>(dev, s))
-                                  : (f32 ? paged_attn_slots<64, true>(dev, s) : paged_attn_slots<64, false>(dev, s));
+    const int reach = shape == 1 ? 16 : 8;               // chunks in which a stream sees 1024 keys
+    const int least = f32 ? std::min(md::attn_paged::kMaxSplits, (chunks + reach - 1) / reach) : 1;
+    for (int s = least; s <= (shape == 0 ? 1 : md::attn_paged::kMaxSplits) && s <= chunks; ++s) {
+      const int slots = slots_of(streams, s);
       if (slots < s) continue;
       const int per_cta = (chunks + s - 1) / s;
       const double slow = f32 ? 2.0 : 1.0;
-      const double one = per_cta * slow * (tiles > 1 ? 1.1 : 0.8) + 8.0 + (s > 1 ? 0.5 : 0.0);
+      const double one = per_cta * slow * (shape == 0 ? 1.9 : tiles > 1 ? 1.1 : 0.8) + 8.0 + (s > 1 ? 0.5 : 0.0);
       const double two = per_cta * slow * 1.75 + 10.0 + (s > 1 ? 1.5 : 0.0);
       const double longest = tpu == 2 ? two : one;
       const double all = tpu == 2 ? (tiles / 2) * two + (tiles % 2) * one : tiles * one;   // a KV head's units, one split
@@ -984,6 +1001,7 @@ PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, i
       if (best == 0 || us < best) {
         best = us;
         p.tpu = tpu;
+        p.streams = streams;
         p.units = units;
         p.splits = s;
         p.sort = B > 1 && B <= 256 && waves;   // ranking costs B^2 / 640 steps a CTA; many requests even out
@@ -993,7 +1011,7 @@ PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, i
   return p;
 }
 
-template <int DH, bool F32>
+template <int DH, bool F32, int STREAMS>
 md_status launch_attn_paged(const md::attn_paged::Args& a, const md_bf16* q, const md_bf16* k_pages,
                             const md_tree* tree, cudaStream_t st) {
   using namespace md::attn_paged;
@@ -1017,11 +1035,11 @@ md_status launch_attn_paged(const md::attn_paged::Args& a, const md_bf16* q, con
   const uint64_t heads = uint64_t(a.pool) * a.Hkv;
   if ((s = make_map_3d_sw128(&kmap, k_pages, DH, a.page, heads, 64, a.piece)) != MD_OK) return s;
   if ((s = make_map_3d_sw128(&vmap, a.v_pages, DH, a.page, heads, 64, a.piece)) != MD_OK) return s;
-  if ((s = paged_attn_attributes<DH, F32>()) != MD_OK) return s;
+  if ((s = paged_attn_attributes<DH, F32, STREAMS>()) != MD_OK) return s;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  paged_attn_config<DH, F32>(&cfg, attr, dim3(a.splits, a.Hkv * a.units, a.B), st);
-  return cuda_ok(cudaLaunchKernelEx(&cfg, attn_paged_kernel<DH, F32>, qmap, kmap, vmap, tree->tp, a));
+  paged_attn_config<DH, F32, STREAMS>(&cfg, attr, dim3(a.splits, a.Hkv * a.units, a.B), st);
+  return cuda_ok(cudaLaunchKernelEx(&cfg, attn_paged_kernel<DH, F32, STREAMS>, qmap, kmap, vmap, tree->tp, a));
 }
 
 // ----------------------------- Hydra planning ------------------------------
@@ -1642,15 +1660,16 @@ md_status md_tree_attention_paged(const md_bf16* q, const md_bf16* k_pages, cons
   md::attn_paged::Args a;
   a.v_pages = v_pages; a.table = block_table; a.prefix_len = prefix_len; a.out = out;
   a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.pool = pool_pages; a.page = page_size; a.max_pages = max_pages;
-  a.piece = std::min(page_size & -page_size, md::attn_paged::kBN);
+  a.piece = std::min(page_size & -page_size, 64 * pl.streams);   // rows of a TMA copy, within a chunk
   a.tpt = pl.tpt; a.tpu = pl.tpu; a.units = pl.units; a.splits = pl.splits; a.sort = pl.sort;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt(float(dh))) * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (out_type == MD_OUT_F32)
-    return dh == 128 ? launch_attn_paged<128, true>(a, q, k_pages, tree, st)
-                     : launch_attn_paged<64, true>(a, q, k_pages, tree, st);
-  return dh == 128 ? launch_attn_paged<128, false>(a, q, k_pages, tree, st)
-                   : launch_attn_paged<64, false>(a, q, k_pages, tree, st);
+  const bool f32 = out_type == MD_OUT_F32, one = pl.streams == 1;
+  auto launch = dh == 128 ? (f32 ? (one ? launch_attn_paged<128, true, 1> : launch_attn_paged<128, true, 2>)
+                                 : (one ? launch_attn_paged<128, false, 1> : launch_attn_paged<128, false, 2>))
+                          : (f32 ? (one ? launch_attn_paged<64, true, 1> : launch_attn_paged<64, true, 2>)
+                                 : (one ? launch_attn_paged<64, false, 1> : launch_attn_paged<64, false, 2>));
+  return launch(a, q, k_pages, tree, st);
 }
 
 md_status md_qk_rope_append(const md_bf16* q, const md_bf16* k, const md_bf16* v, const int64_t* strides,

@@ -577,6 +577,70 @@ def test_more_units_than_one_wave(B, T, Hq, Hkv, page, P):
     _check_attention(out, q, kp, vp, table, lens, parent)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,dh,page,longest", [(170, 1, 4, 1, 128, 16, 300), (90, 7, 6, 2, 64, 48, 200),
+                                                        (80, 17, 8, 4, 128, 64, 150), (160, 64, 2, 1, 64, 16, 130),
+                                                        (150, 64, 1, 1, 128, 128, 90), (150, 64, 8, 1, 128, 32, 90)])
+def test_many_short_requests(B, T, Hq, Hkv, dh, page, longest, dtype):
+    """More CTAs than SMs, few keys each. Slots that no request uses hold NaN, and the
+    last node's V is infinite in one column: that reaches the node's own rows alone."""
+    rng = np.random.default_rng(B + T)
+    parent, rank = _tree(T - 1)
+    lens = [int(x) for x in rng.integers(0, longest, B)]
+    lens[:8] = [0, -1, 63, 64, 65, 1, 127, 128 - T if T < 128 else 0]
+    lens = [min(p, longest) for p in lens]
+    table, pool = _table(rng, lens, T, page)
+    q = gen.normal_bf16(6, "q", (B, T, Hq, dh), 1.0)
+    k = gen.normal_bf16(6, "k_cache", (pool, Hkv, page, dh), 1.0)
+    v = gen.normal_bf16(6, "v_cache", (pool, Hkv, page, dh), 1.0)
+    kp, vp = np.full_like(k, NAN), np.full_like(v, NAN)
+    for b, p in enumerate(lens):
+        for s in range(p + T if p >= 0 else 0):
+            at = (table[b, s // page], slice(None), s % page)
+            kp[at], vp[at] = k[at], v[at]
+    args = (bf16_tensor(q), bf16_tensor(kp), bf16_tensor(vp), i32(table), i32(lens), parent, rank, dtype)
+    md.device_status(clear=True)
+    out, again = _attention(*args), _attention(*args)
+    assert md.device_status() == 0
+    _check_attention(out, q, kp, vp, table, lens, parent)
+    assert torch.equal(out, again) and not out[1].any()
+    if T > 1:
+        inf = vp.copy()
+        for b, p in enumerate(lens):
+            if p >= 0:
+                inf[table[b, (p + T - 1) // page], :, (p + T - 1) % page, 5] = 0x7F80
+        bad = _attention(args[0], args[1], bf16_tensor(inf), *args[3:])
+        live = [b for b in range(B) if lens[b] >= 0]
+        assert torch.isinf(bad[live, T - 1, :, 5]).all()
+        bad[:, T - 1, :, 5] = out[:, T - 1, :, 5]
+        assert torch.equal(bad, out)
+
+
+def test_many_short_requests_timeout_flags_and_recovers():
+    rng = np.random.default_rng(4)
+    parent, rank = _tree(4)
+    for P, chunk in ((300, 1), (40, 0)):
+        B, T, Hq, Hkv, dh, page = 170, 5, 4, 1, 64, 16
+        table, pool = _table(rng, [P] * B, T, page)
+        q = gen.normal_bf16(8, "q", (B, T, Hq, dh), 1.0)
+        kp = gen.normal_bf16(8, "k_cache", (pool, Hkv, page, dh), 1.0)
+        vp = gen.normal_bf16(8, "v_cache", (pool, Hkv, page, dh), 1.0)
+        args = [bf16_tensor(q), bf16_tensor(kp), bf16_tensor(vp), i32(table), i32([P] * B), parent, rank, torch.bfloat16]
+        good = _attention(*args)
+        md.device_status(clear=True)
+        md.set_wait_limit(1_000_000)
+        md.binding.withhold_attention_chunk_for_test(chunk)
+        try:
+            _attention(*args)
+            torch.cuda.synchronize()
+            status = md.device_status(clear=True)
+        finally:
+            md.binding.withhold_attention_chunk_for_test(-1)
+            md.set_wait_limit(0)
+        assert status & md.binding.DEV_TIMEOUT
+        assert torch.equal(_attention(*args), good) and md.device_status() == 0
+
+
 def test_scores_far_apart_and_rows_of_nan():
     """Maxima that climb by thousands from chunk to chunk (the running maximum moves,
     the result is rescaled), a prefix key of NaN, and a query of NaN."""
