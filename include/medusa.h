@@ -535,9 +535,9 @@ MD_API md_status md_attention_paged_workspace(int32_t B, int32_t T, int32_t Hq, 
  *         read as zeros.
  * scale   softmax scale; 0 means 1/sqrt(dh).
  * out     [B, T, Hq, dh] fp32 (MD_OUT_F32; weights kept to 24 bits, sums of at most
- *         1024 keys in the tensor cores up to 32768 slots: off by a few 1e-6 of the
- *         result there, less where shorter) or bf16 (MD_OUT_BF16; weights rounded to
- *         bf16, about twice as fast over long prefixes).
+ *         128 keys in the tensor cores: off by less than 1e-6 of the result) or bf16
+ *         (MD_OUT_BF16; weights rounded to bf16, about twice as fast over long
+ *         prefixes).
  * q, k_pages, v_pages and out 16-byte aligned; out not q. The workspace is
  * md_attention_paged_workspace()'s, 256-byte aligned, with any contents.
  * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_WORKSPACE, MD_ERR_CUDA. */

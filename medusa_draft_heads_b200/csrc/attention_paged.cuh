@@ -34,7 +34,10 @@
 // error, at most 2^-8 of it either way, averages out over the keys, and the result is
 // rounded to the same precision (0.0023 of the result against 64 bits, 0.0017 being
 // the last rounding's own). For fp32 results P is three bf16 parts, 24 bits, and P V
-// three products; S then has one buffer, the parts needing the other's columns.
+// three products; S then has one buffer, the parts needing the other's columns. The
+// tensor cores' accumulator drops what it cannot hold at every step (8e-6 of the result
+// over 20000 keys), so after every 128 keys O is added to a sum in local memory:
+// at most 8e-7 of the result at any length (256 keys a stretch 1.2e-6, 192 1.0e-6).
 //
 // The KV splits of a unit are the CTAs of a cluster: O and (m, sum) of every
 // stream are staged in shared memory, and each CTA combines its share of the
@@ -57,6 +60,8 @@
 // about 8 us, are as much as the walk (70B tree over 4096 slots: 22.5 us). Many
 // requests of few keys: the same fixed part once a CTA, halved by two CTAs an SM.
 #pragma once
+
+#include <climits>
 
 #include "attention_tc.cuh"
 #include "common.cuh"
@@ -88,6 +93,9 @@ struct Cfg {
   // job ends; fp32 ones: the three parts of P take the columns of the second
   static constexpr int kBufs = F32 ? 1 : 2;
   static constexpr int kParts = F32 ? 3 : 1;               // bf16 parts of P
+  // jobs (of 64 keys) in one accumulator; fp32 results: then it is added to a sum
+  // outside the tensor cores, whose accumulator drops what it cannot hold at every step
+  static constexpr int kStretch = F32 ? 2 : INT_MAX;
   static constexpr int KB = DH / 64;                       // 64-column blocks
   static constexpr uint32_t kQTile = KB * kBM * 128;       // 128 rows x DH bf16, 128-byte swizzle
   static constexpr uint32_t kTile = KB * kBN * 128;        // a chunk of K or V
@@ -512,7 +520,7 @@ __global__ void __launch_bounds__(Cfg<DH, F32, STREAMS>::kThreads, 3 - STREAMS)
 #pragma unroll
             for (int kk = 0; kk < kSub / 16; ++kk)
               umma_f16_tmem_a_elect(tO, tS + buf * kSub + uint32_t(part * (kSub / 2) + kk * 8), bd + uint64_t((kk * 2048) >> 4),
-                                    idesc_o, (part | kk) != 0 ? 1u : uint32_t(j > 0));
+                                    idesc_o, (part | kk) != 0 ? 1u : uint32_t(j % C::kStretch != 0));
           umma_commit_elect(smem_u32(&o_full[w]));
           if (TILES == 1 || half == 1 || j == jobs - 1) {
             umma_commit_elect(smem_u32(&v_empty[vs]));
@@ -574,6 +582,10 @@ __global__ void __launch_bounds__(Cfg<DH, F32, STREAMS>::kThreads, 3 - STREAMS)
     const float sc = a.scale_log2;
     const int my_jobs = two || !kPair ? nsub : (nsub - w + 1) / 2;
     float run_m = -INFINITY, run_l = 0.f;
+    // fp32 results: the finished stretches' sum, this thread's half of the row (indexed
+    // in rolled loops: local memory), against the maximum keep_m
+    [[maybe_unused]] float keep[F32 ? DH / 2 : 1];
+    [[maybe_unused]] float keep_m = -INFINITY;
     bool ok = true;
     for (int j = 0; j < my_jobs; ++j) {
       const int u = two || !kPair ? j : 2 * j + w;       // 64 keys of the range
@@ -584,6 +596,21 @@ __global__ void __launch_bounds__(Cfg<DH, F32, STREAMS>::kThreads, 3 - STREAMS)
       const uint32_t tSb = tS + buf * kSub;
       const int key0 = c_begin * kBN + u * kSub;
       if (warp_live) {
+        if constexpr (F32) {
+          if (j > 0 && j % C::kStretch == 0 && ok) {
+            // S of this job was issued behind the last P V: O is complete, and the next
+            // P V, which overwrites it, waits for this job's P
+            const float f = keep_m == -INFINITY || keep_m == run_m ? 1.f : exp2f(keep_m - run_m);
+            keep_m = run_m;
+#pragma unroll 1
+            for (int e0 = 0; e0 < DH / 2; e0 += 16) {
+              float o[16];
+              tmem_ld16(tO + half * (DH / 2) + e0, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) keep[e0 + e] = j == C::kStretch ? o[e] : fmaf(keep[e0 + e], f, o[e]);
+            }
+          }
+        }
         float s[32];
         if (ok) tmem_ld32_async(tSb + half * 32, s);
         tmem_ld_wait();
@@ -703,6 +730,13 @@ __global__ void __launch_bounds__(Cfg<DH, F32, STREAMS>::kThreads, 3 - STREAMS)
       for (int e0 = half * (DH / 2); e0 < (half + 1) * (DH / 2); e0 += 16) {
         float o[16];
         tmem_ld16(tO + e0, o);
+        if constexpr (F32) {
+          if (my_jobs > C::kStretch) {
+            const float f = keep_m == -INFINITY || keep_m == run_m ? 1.f : exp2f(keep_m - run_m);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(keep[e0 - half * (DH / 2) + e], f, o[e]);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
           float4* to = reinterpret_cast<float4*>(sO + e0 + e);

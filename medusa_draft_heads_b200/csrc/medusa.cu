@@ -951,7 +951,7 @@ struct PagedAttnPlan {
 //     22.6. 16 requests of 26000: 1 split 261, 2 276; of 20001 to 32768: 316, 270.
 //   One stream against two, 32/8 heads, one node: 256 requests of 200 slots 105 against
 //     189, of 2000 365 against 446; 64 of 200 20.7 against 41.7; 32 of 500 13.2 against
-//     24.9; 64 of 17 nodes over 200 33.9 against 53.3, fp32 47.1 against 63.6.
+//     24.9; 64 of 17 nodes over 200 33.9 against 53.3, 256 of 200 in fp32 158 against 223.
 PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, int max_pages, bool f32) {
   PagedAttnPlan p;
   const int G = Hq / Hkv;
@@ -980,13 +980,7 @@ PagedAttnPlan paged_attn_plan(int B, int T, int Hq, int Hkv, int dh, int page, i
     const int tpu = std::max(shape, 1), streams = shape == 0 ? 1 : 2;
     const int units = (tiles + tpu - 1) / tpu;
     const int64_t base = int64_t(B) * Hkv * units;
-    // An accumulator of the tensor cores drops what it cannot hold at every step, which
-    // over thousands of keys shows in fp32 results (8e-6 at 20000 keys of a stream, 7e-7 at
-    // 1024): those are summed in stretches of at most 1024 keys a stream, as far as 16
-    // splits reach.
-    const int reach = shape == 1 ? 16 : 8;               // chunks in which a stream sees 1024 keys
-    const int least = f32 ? std::min(md::attn_paged::kMaxSplits, (chunks + reach - 1) / reach) : 1;
-    for (int s = least; s <= (shape == 0 ? 1 : md::attn_paged::kMaxSplits) && s <= chunks; ++s) {
+    for (int s = 1; s <= (shape == 0 ? 1 : md::attn_paged::kMaxSplits) && s <= chunks; ++s) {
       const int slots = slots_of(streams, s);
       if (slots < s) continue;
       const int per_cta = (chunks + s - 1) / s;
