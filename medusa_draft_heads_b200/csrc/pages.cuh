@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kThreads) pages_resize_kernel(ResizeArgs a) {
     const int b = b0 + threadIdx.x;
     int need = 0;
     if (b < a.B) {
-      const int held = a.n_pages[b];
-      need = max(0, wanted_pages(a, b, held) - held);
+      const int held = a.n_pages[b], want = wanted_pages(a, b, held);
+      need = want < 0 ? 0 : max(0, want - held);   // a row left alone: its count may be anything
     }
     int total;
     const int incl = block_incl_scan(need, part, total);

@@ -474,6 +474,34 @@ def test_resize_leaves_impossible_rows_alone():
     assert md.device_status(clear=True) == md.binding.DEV_BAD_PREFIX and g[1].cpu().tolist() == [0]
 
 
+def test_resize_leaves_rows_with_negative_counts_alone():
+    """Counts below zero: nothing is given to such a row, nothing written through it. The
+    table lies between guard rows, as a row's first entry minus its count would reach them."""
+    width, pool = 4, 12
+    counts = [-5, -1, 2, -2, -2 ** 31, 1, -2 ** 31 + 1, -5]
+    B = len(counts)
+    full = np.full((B + 8, width), 77, dtype=np.int32)
+    table = full[4:4 + B]
+    table[:] = 33                                          # what a row with a bad count holds means nothing
+    table[2], table[5] = [0, 1, -1, -1], [2, -1, -1, -1]
+    ref = np.array([1, 1, 1] + [0] * (pool - 3), dtype=np.int32)
+    length = [64, 1, 48, 64, 64, 64, 0, -1]
+    gfull, gn, gref = i32(full), i32(counts), i32(ref)
+    md.device_status(clear=True)
+    md.pages_resize(gfull[4:4 + B], gn, gref, i32(length), 16)
+    assert md.device_status(clear=True) == md.binding.DEV_BAD_PAGE
+    rt, rn, rr, short = op.pages_resize(table, np.array(counts), ref, np.array(length), 16)
+    assert not short and rn.tolist() == [-5, -1, 3, -2, -2 ** 31, 4, -2 ** 31 + 1, -5]
+    full[4:4 + B] = rt
+    assert np.array_equal(gfull.cpu().numpy(), full)
+    assert gn.cpu().tolist() == rn.tolist() and np.array_equal(gref.cpu().numpy(), rr)
+    # one row alone, the first of its table; the pool is not drained
+    gfull, gn, gref = i32(np.full((3, width), 77)), i32([-5]), i32(np.zeros(pool))
+    md.pages_resize(gfull[1:2], gn, gref, i32([64]), 16, extra=16)
+    assert md.device_status(clear=True) == md.binding.DEV_BAD_PAGE
+    assert (gfull == 77).all() and gn.item() == -5 and not gref.any()
+
+
 @pytest.mark.parametrize("layers,Hkv,dh,page,B,n", [(1, 1, 64, 16, 6, 2), (3, 2, 128, 7, 9, 4), (2, 8, 128, 64, 40, 19)])
 def test_fork_matches_oracle(layers, Hkv, dh, page, B, n):
     rng = np.random.default_rng(page + n)

@@ -114,3 +114,12 @@ def test_resize_and_fork_conserve_pages():
                 own = length[s] // page
                 assert n[d] == own or ref[table[d, own]] == 1        # the page the sequence goes on in is its own
     assert ref.max() > 1                                             # pages were shared
+
+
+def test_resize_serves_no_row_whose_count_is_impossible():
+    table = np.array([[33, 33], [0, -1], [33, 33], [33, 33]], dtype=np.int32)
+    n = np.array([-2 ** 31, 1, -2, 3], dtype=np.int32)
+    ref = np.array([1, 0, 0, 0], dtype=np.int32)
+    t2, n2, r2, short = op.pages_resize(table, n, ref, np.array([32, 32, 32, 32]), 16)
+    assert not short and t2.tolist() == [[33, 33], [0, 1], [33, 33], [33, 33]]
+    assert n2.tolist() == [-2 ** 31, 2, -2, 3] and r2.tolist() == [1, 1, 0, 0]
