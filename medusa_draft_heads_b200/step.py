@@ -114,6 +114,9 @@ class MedusaStep:
         self.accept(logits, stream)
 
 
+MAX_FORKS = 1024   # entries of one pages_fork call
+
+
 class PagedMedusaStep(MedusaStep):
     """The step over a KV cache held in pages.
 
@@ -143,7 +146,8 @@ class PagedMedusaStep(MedusaStep):
         self.refcount = torch.zeros((pool_pages,), **i32)
         self.attn_out = torch.empty((self.B, self.T, self.Hq, self.dh), dtype=out_dtype, device=dev)
         self.q = torch.empty((self.B, self.T, self.Hq, self.dh), dtype=torch.bfloat16, device=dev)
-        self.ws_fork = None
+        # for the largest call, and never replaced: a captured graph keeps its address
+        self.ws_fork = workspace(pages_fork_workspace_bytes(self.B, MAX_FORKS), dev)
 
     def _attention_workspace_bytes(self):
         return attention_paged_workspace_bytes(self.B, self.T, self.Hq, self.Hkv, self.dh, self.page_size, self.max_pages)
@@ -178,9 +182,7 @@ class PagedMedusaStep(MedusaStep):
                           self.bonus, self.new_prefix_len, self.next_root, self.next_head_row, stream=stream)
 
     def fork(self, k_pages, v_pages, src, dst, prefix_len, stream=None):
-        """Rows dst continue the sequences of rows src; prefix_len[dst] is set."""
-        n = src.shape[0]
-        if self.ws_fork is None or self.ws_fork.numel() < pages_fork_workspace_bytes(self.B, n):
-            self.ws_fork = workspace(pages_fork_workspace_bytes(self.B, n), self.tokens.device)
+        """Rows dst continue the sequences of rows src; prefix_len[dst] is set. At most
+        MAX_FORKS entries a call."""
         pages_fork(k_pages, v_pages, self.block_table, self.n_pages, self.refcount, src, dst, prefix_len, self.ws_fork,
                    stream=stream)

@@ -157,3 +157,22 @@ def test_paged_step_is_a_medusa_step():
     assert issubclass(PagedMedusaStep, MedusaStep)
     for name in ("prefill_pages", "reserve", "append", "attention", "commit", "trim", "fork"):
         assert callable(getattr(PagedMedusaStep, name))
+
+
+def test_fork_workspace_stays_where_it_is(monkeypatch):
+    """A graph that captured a fork keeps the workspace's address: calls of any size use the same one."""
+    from medusa_draft_heads_b200 import step as step_module
+    seen = []
+
+    def fork(kp, vp, table, n_pages, refcount, src, dst, length, ws, stream=None):
+        assert ws.numel() >= md.pages_fork_workspace_bytes(B, src.shape[0])
+        seen.append((ws.data_ptr(), ws.numel()))
+
+    monkeypatch.setattr(step_module, "pages_fork", fork)
+    step = PagedMedusaStep(B=B, M=B, d=256, V=2048, K=4, k_per_head=(4, 3, 2, 2), Hq=Hq, Hkv=Hkv, dh=dh, page_size=page,
+                           tree_tuples=md.select_tree((4, 3, 2, 2), TREE_ACCEPT, 16), max_pages=width, pool_pages=pages,
+                           device="cpu")
+    pool = bf(1, pages, Hkv, page, dh)
+    for n in (1, 16, 17, 1, 1024):
+        step.fork(pool, pool, i32(n), i32(n), i32(B))
+    assert len(set(seen)) == 1

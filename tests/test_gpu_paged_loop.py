@@ -134,3 +134,34 @@ def test_paged_decode_loop_matches_oracle():
         P, root = P2.astype(np.int32), np.maximum(root2, 0).astype(np.int32)
     # the fork's sequences went on in pages of their own, sharing the first
     assert ref.max() == 2 and table[0, 0] == table[3, 0] and table[0, 2] != table[3, 2]
+
+
+def test_a_captured_fork_replays_after_larger_ones():
+    """A fork of one row captured, then eager forks of many rows and other allocations, then the graph again."""
+    B, Hkv, dh, page, width, pool = 48, 2, 64, 16, 4, 200
+    kph = (4, 3, 2, 2)
+    step = PagedMedusaStep(B=B, M=B, d=256, V=2048, K=4, k_per_head=kph, tree_tuples=md.select_tree(kph, TREE_ACCEPT, 16), Hq=4,
+                           Hkv=Hkv, dh=dh, page_size=page, max_pages=width, pool_pages=pool, out_dtype=torch.bfloat16)
+    k = gen.normal_bf16(1, "k_cache", (2, pool, Hkv, page, dh), 1.0)
+    v = gen.normal_bf16(1, "v_cache", (2, pool, Hkv, page, dh), 1.0)
+    gk, gv = bf16_tensor(k), bf16_tensor(v)
+    length = np.full(B, -1, dtype=np.int32)
+    length[:20] = 17 + np.arange(20)
+    table, cnt, ref = np.full((B, width), -1, np.int32), np.zeros(B, np.int32), np.zeros(pool, np.int32)
+    glen, one = i32(length), (i32([3]), i32([47]))
+    step.prefill_pages(glen)
+    table, cnt, ref, _ = op.pages_resize(table, cnt, ref, length, page)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step.fork(gk, gv, *one, glen)
+    many = np.arange(20), np.arange(20) + 20
+    step.fork(gk, gv, i32(many[0]), i32(many[1]), glen)
+    k, v, table, cnt, ref, length = op.pages_fork(k, v, table, cnt, ref, *many, length)
+    junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in (256, 512, 1024, 16384) for _ in range(8)]
+    g.replay()
+    k, v, table, cnt, ref, length = op.pages_fork(k, v, table, cnt, ref, np.array([3]), np.array([47]), length)
+    assert md.device_status() == 0
+    assert np.array_equal(to_bits(gk), k) and np.array_equal(to_bits(gv), v)
+    for got, want in ((step.block_table, table), (step.n_pages, cnt), (step.refcount, ref), (glen, length)):
+        assert np.array_equal(got.cpu().numpy(), want)
+    assert all(bool((x == 0x7F).all()) for x in junk)
