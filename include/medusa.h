@@ -585,7 +585,8 @@ MD_API md_status md_qk_rope_append(const md_bf16* q, const md_bf16* k, const md_
  * k_pages, v_pages [layers, pool_pages, Hkv, page_size, dh] bf16, updated in
  * place; the other arguments and results are md_tree_commit's. An idle slot
  * gives -1, -1, -1. A bad length, path or prefix (MD_DEV_BAD_PATH), or a bad
- * page under a row that moves (MD_DEV_BAD_PAGE), leaves that request's cache
+ * page under an accepted node, the root included (MD_DEV_BAD_PAGE: its K/V were
+ * never written, as after a resize that ran short), leaves that request's cache
  * unchanged (new_prefix_len = P, next_head_row = -1).
  * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED (dh not 64/128), MD_ERR_CUDA. */
 MD_API md_status md_tree_commit_paged(md_bf16* k_pages, md_bf16* v_pages, int32_t layers, int32_t pool_pages,

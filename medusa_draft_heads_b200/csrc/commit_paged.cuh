@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kThreads) tree_commit_paged_kernel(const __gri
       } else {
         const int32_t* row = a.table + size_t(b) * a.max_pages;
         const int sp = row[(P + n) / a.page], dp = row[(P + i) / a.page];
-        // pages matter only for a row that moves
-        if (n != i && (sp < 0 || sp >= a.pool || dp < 0 || dp >= a.pool)) bad = MD_DEV_BAD_PAGE;
+        // also for a row in place: without a page its K/V were never written
+        if (sp < 0 || sp >= a.pool || dp < 0 || dp >= a.pool) bad = MD_DEV_BAD_PAGE;
         from[i] = (long long)sp * a.Hkv * a.page + (P + n) % a.page;
         to[i] = (long long)dp * a.Hkv * a.page + (P + i) % a.page;
         node[i] = n;

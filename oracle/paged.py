@@ -80,7 +80,8 @@ def qk_rope_append(q, k, v, pos, inv_freq, table, prefix_len, pool_shape, q_norm
 
 
 def tree_commit_paged(k_pages, v_pages, table, prefix_len, accept_len, path, bonus, T):
-    """Pools [layers, pages, Hkv, page, dh]; returns copies and the next step's inputs."""
+    """Pools [layers, pages, Hkv, page, dh]; returns copies and the next step's inputs. A request
+    with an accepted node in no page of the pool stays as it is."""
     k, v = k_pages.copy(), v_pages.copy()
     page = k.shape[3]
     newp, root, row = [], [], []
@@ -88,6 +89,10 @@ def tree_commit_paged(k_pages, v_pages, table, prefix_len, accept_len, path, bon
         P, L = int(prefix_len[b]), int(accept_len[b])
         if P == -1:
             newp.append(-1), root.append(-1), row.append(-1)
+            continue
+        slots = [P + int(path[b, i]) for i in range(L + 1)] + list(range(P, P + L + 1))
+        if not all(0 <= table[b, s // page] < k.shape[1] for s in slots):
+            newp.append(P), root.append(int(bonus[b])), row.append(-1)
             continue
         for i in range(L + 1):
             s, d = P + int(path[b, i]), P + i

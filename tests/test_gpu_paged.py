@@ -426,6 +426,38 @@ def test_commit_leaves_bad_requests_alone():
     assert outs[1].cpu().tolist() == [1, 2, 3, 4]
 
 
+def test_commit_refuses_nodes_without_a_page():
+    """A resize that ran short leaves rows without pages for their tree: nothing of theirs is
+    accepted, not even what would stay where it is, and the next resize frees no foreign slots."""
+    parent, rank = [-1, 0, 0, 1], [0, 0, 1, 0]
+    T, page, pool, width = 4, 16, 5, 3
+    tree = md.Tree(parent, rank, [2, 1])
+    table, n, ref = _state(4, width, pool)
+    P = np.array([16, 31, 16, -1], dtype=np.int32)
+    g = [i32(x) for x in (table, n, ref)]
+    md.device_status(clear=True)
+    md.pages_resize(*g, i32(P), page)
+    md.pages_resize(*g, i32(P), page, extra=T)                 # three rows need one more page each, one is left
+    assert md.device_status(clear=True) == md.binding.DEV_NO_PAGES
+    held = g[0].cpu().numpy()
+    assert g[1].cpu().tolist() == [2, 2, 1, 0]
+    k0 = gen.normal_bf16(1, "k_cache", (2, pool, 1, page, 64), 1.0)
+    kp, vp = bf16_tensor(k0), bf16_tensor(k0)
+    ref_k = k0
+    bonus = [1, 2, 3, 4]
+    # paths of the root alone; of nodes in place; moved ones. Row 1's root has a page, its node 1 none.
+    for L, path in (([0, 0, 0, 0], [[0, -1, -1]] * 4), ([1] * 4, [[0, 1, -1]] * 4), ([2] * 4, [[0, 1, 3]] * 4)):
+        outs = [torch.zeros(4, dtype=torch.int32, device="cuda") for _ in range(3)]
+        md.tree_commit_paged(kp, vp, g[0], tree, i32(P), i32(L), i32(path), i32(bonus), *outs)
+        assert md.device_status(clear=True) == md.binding.DEV_BAD_PAGE
+        ref_k, _, newp, root, row = op.tree_commit_paged(ref_k, ref_k, held, P, L, np.array(path), bonus, T)
+        assert newp.tolist() == [17 + L[0], 32 if L[0] == 0 else 31, 16, -1]
+        assert [x.cpu().tolist() for x in outs] == [newp.tolist(), root.tolist(), row.tolist()]
+        assert np.array_equal(to_bits(kp), ref_k) and np.array_equal(to_bits(vp), ref_k)
+    md.pages_resize(*g, outs[0], page)                         # trim: the refused rows keep what their prefixes need
+    assert md.device_status(clear=True) == 0 and g[1].cpu().tolist() == [2, 2, 1, 0]
+
+
 # -------------------------------------------------------------------- pages
 
 def _state(B, width, pool):

@@ -79,6 +79,17 @@ def test_append_skips_padding_idle_rows_and_slots_without_a_page():
     assert sorted(w) == [(1, 0), (3, 14), (3, 15)]     # request 2: slots 30, 31 in a page outside the pool, 32 and 33 past the table
 
 
+def test_commit_keeps_a_request_without_pages_as_it_is():
+    k = gen.normal_bf16(3, "k_cache", (1, 4, 1, 4, 64), 1.0)
+    table = np.array([[0, -1], [1, 9], [2, 3]])
+    # row 0: the root has a page at first, its child none; row 1: a page outside the pool
+    for P, L, path, newp, row in (([3, 4, 4], 0, [0, -1], [4, 4, 5], [0, -1, 8]), ([3, 4, 4], 1, [0, 1], [3, 4, 6], [-1, -1, 9]),
+                                  ([4, 4, 4], 0, [0, -1], [4, 4, 5], [-1, -1, 8])):
+        k2, _, got, root, head = op.tree_commit_paged(k, k, table, P, [L] * 3, np.array([path] * 3), [1, 2, 3], 4)
+        assert got.tolist() == newp and root.tolist() == [1, 2, 3] and head.tolist() == row
+        assert np.array_equal(k2, k)                            # nothing moves on these paths
+
+
 def _consistent(table, n_pages, ref):
     count = np.zeros_like(ref)
     for b in range(len(n_pages)):
