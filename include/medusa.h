@@ -270,7 +270,9 @@ MD_API md_status md_medusa_heads_static(const md_bf16* h, const md_bf16* W1, con
  * root_token [B] int32.  prefix_len [B] int32.
  * tokens [B, T] int32, parent [T] int32, anc [T, W] uint32, pos [B, T] int32.
  * A head_row outside [0, M) sets MD_DEV_BAD_ROW and that request's candidate
- * tokens are -1. Errors: MD_ERR_INVALID_ARG, MD_ERR_CUDA. */
+ * tokens are -1. prefix_len[b] = -1 marks an idle row of a padded batch: its tokens
+ * are 0, pos[b,j] = depth(j), its root_token and head_row are not looked at.
+ * Errors: MD_ERR_INVALID_ARG, MD_ERR_CUDA. */
 MD_API md_status md_tree_build(const md_tree* tree, const int32_t* topk_ids, int32_t M, int32_t kmax,
                         const int32_t* head_row, const int32_t* root_token, const int32_t* prefix_len,
                         int32_t B, int32_t* tokens, int32_t* parent, uint32_t* anc, int32_t* pos,
@@ -320,7 +322,8 @@ MD_API md_status md_hydra_workspace(const md_tree* tree, int32_t B, int32_t d, i
  * ws, ws_bytes: workspace of at least md_hydra_workspace() bytes, 256-byte aligned.
  * A head_row outside [0, M) sets MD_DEV_BAD_ROW (that request's head inputs
  * use a zero hidden state); a drafted token outside [0, V) sets
- * MD_DEV_BAD_TOKEN (its embedding counts as zero).
+ * MD_DEV_BAD_TOKEN (its embedding counts as zero). An idle row (prefix_len[b] =
+ * -1) gives what md_tree_build gives for it; its head inputs are zeros.
  * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED (sizes md_medusa_heads does
  * not take for one head on B * n_l rows), MD_ERR_WORKSPACE, MD_ERR_CUDA. */
 MD_API md_status md_hydra_draft(const md_tree* tree, const md_bf16* h, int32_t M, const int32_t* head_row,
@@ -453,9 +456,9 @@ MD_API md_status md_tree_accept_sampled(const float* logits, int32_t V, const in
  * otherwise); K >= tree depth, Kh >= tree depth; V <= 196,608. One 8-CTA
  * cluster per request; no workspace. Decisions are taken in fp32 with a fixed
  * summation order: a uniform within ~1e-5 (relative) of its threshold or CDF
- * boundary may resolve differently from exact arithmetic. A head row outside
- * [0, M) (MD_DEV_BAD_ROW) accepts nothing; a token outside [0, V)
- * (MD_DEV_BAD_TOKEN) is rejected.
+ * boundary may resolve differently from exact arithmetic. A head row of -1 (the
+ * commit's of an idle or refused request) accepts nothing; so does any other outside
+ * [0, M) (MD_DEV_BAD_ROW); a token outside [0, V) (MD_DEV_BAD_TOKEN) is rejected.
  * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_CUDA. */
 MD_API md_status md_tree_accept_rejection(const float* logits, int32_t V, const int32_t* tokens,
                                           const md_tree* tree, int32_t B, int32_t K, float temperature,
@@ -512,8 +515,10 @@ MD_API md_status md_tree_commit(md_bf16* k_cache, md_bf16* v_cache, int32_t S_ma
  *
  * In every call prefix_len[b] = -1 marks an idle slot of a padded batch: its
  * attention output is zero, the other outputs are as each call says, nothing is
- * read or written through its row of the table, and no status bit is set. A
- * page id outside [0, pool_pages) where one is needed sets MD_DEV_BAD_PAGE. */
+ * read or written through its row of the table, and no status bit is set. What
+ * the commit gives for it (-1, -1, -1) goes back into the step as it is: md_tree_build
+ * and the acceptance calls take it for an idle row. A page id outside
+ * [0, pool_pages) where one is needed sets MD_DEV_BAD_PAGE. */
 
 /* Output types of md_tree_attention_paged. */
 enum { MD_OUT_F32 = 0, MD_OUT_BF16 = 1 };

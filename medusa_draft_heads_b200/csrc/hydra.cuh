@@ -31,6 +31,7 @@ struct GatherArgs {
   const uint16_t* E;          // [V, d] bf16 input embedding
   const int32_t* head_row;    // [B] or null (row b)
   const int32_t* root_token;  // [B]
+  const int32_t* prefix_len;  // [B]
   const int32_t* prev_ids;    // previous level's top-k ids, its first row (null at level 0)
   uint16_t* x;                // [B * n, d] this level's head inputs
   int M, d, V, kmax;
@@ -57,9 +58,10 @@ __global__ void __launch_bounds__(kGatherThreads) hydra_gather_kernel(const __gr
     tok = a.prev_ids[(size_t(b) * a.n_prev + a.pslot[q]) * a.kmax + a.prank[q]];
   }
   const int row = a.head_row ? a.head_row[b] : b;
-  const bool tok_ok = tok >= 0 && tok < a.V;
-  const bool row_ok = row >= 0 && row < a.M;
-  if (threadIdx.x == 0) {
+  const bool idle = a.prefix_len[b] == -1;   // holds no request: zeros, and nothing to report
+  const bool tok_ok = !idle && tok >= 0 && tok < a.V;
+  const bool row_ok = !idle && row >= 0 && row < a.M;
+  if (threadIdx.x == 0 && !idle) {
     if (!tok_ok) set_status(MD_DEV_BAD_TOKEN);
     if (!row_ok) set_status(MD_DEV_BAD_ROW);
   }
@@ -106,8 +108,12 @@ __global__ void __launch_bounds__(MD_MAX_T) hydra_tokens_kernel(const __grid_con
   const int j = threadIdx.x;
   if (j >= tp.T) return;
   const int d = tp.depth[j];
+  const int P = a.prefix_len[b];
+  const bool idle = P == -1;
   int32_t tok;
-  if (j == 0) {
+  if (idle) {
+    tok = 0;
+  } else if (j == 0) {
     tok = a.root_token[b];
   } else {
     const int l = d - 1;
@@ -116,7 +122,7 @@ __global__ void __launch_bounds__(MD_MAX_T) hydra_tokens_kernel(const __grid_con
     tok = a.ids[row * a.kmax + tp.rank[j]];
   }
   a.tokens[size_t(b) * tp.T + j] = tok;
-  a.pos[size_t(b) * tp.T + j] = a.prefix_len[b] + d;
+  a.pos[size_t(b) * tp.T + j] = (idle ? 0 : P) + d;
   if (b == 0) {
     a.parent[j] = tp.parent[j];
     for (int w = 0; w < tp.W; ++w) a.anc[size_t(j) * tp.W + w] = tp.anc[j][w];

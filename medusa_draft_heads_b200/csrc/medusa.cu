@@ -1378,7 +1378,7 @@ md_status md_hydra_draft(const md_tree* tree, const md_bf16* h, int32_t M, const
   for (int l = 0; l < p.L; ++l) {
     md::hydra::GatherArgs ga;
     std::memset(&ga, 0, sizeof(ga));
-    ga.h = h; ga.E = E; ga.head_row = head_row; ga.root_token = root_token;
+    ga.h = h; ga.E = E; ga.head_row = head_row; ga.root_token = root_token; ga.prefix_len = prefix_len;
     ga.prev_ids = l == 0 ? nullptr : ids + size_t(p.row0[l - 1]) * kmax;
     ga.x = x;
     ga.M = M; ga.d = d; ga.V = V; ga.kmax = kmax;

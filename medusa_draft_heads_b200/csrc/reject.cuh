@@ -41,7 +41,7 @@ constexpr int kSmem = 2 * kMaxSlice * 4;
 struct Args {
   const float* logits;       // target [B, T, V]
   const float* head_logits;  // [M, Kh, V]
-  const int32_t* head_row;   // [B] or null (request b uses row b)
+  const int32_t* head_row;   // [B] or null (request b uses row b); -1: no drafts
   const int32_t* tokens;     // [B, T]
   const float* u_acc;        // [B, T]
   const float* u_res;        // [B, T]
@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1) reject_accept_kernel(const __grid
 
   const int hrow = a.head_row ? a.head_row[b] : b;
   const bool row_ok = hrow >= 0 && hrow < a.M;
-  if (!row_ok && crank == 0 && threadIdx.x == 0) set_status(MD_DEV_BAD_ROW);
+  // -1 is what the commit of an idle or refused request hands on: no drafts, no error of this call
+  if (!row_ok && hrow != -1 && crank == 0 && threadIdx.x == 0) set_status(MD_DEV_BAD_ROW);
 
   int node = 0, depth = 0, L = 0;
   int steps[MD_MAX_K + 1];

@@ -29,16 +29,20 @@ __global__ void __launch_bounds__(MD_MAX_T) tree_build_kernel(const __grid_const
   const int b = blockIdx.x;
   const int j = threadIdx.x;
   __shared__ int row_ok;
+  const int P = a.prefix_len[b];
+  const bool idle = P == -1;   // holds no request: its root and head row mean nothing
   if (j == 0) {
     const int row = a.head_row ? a.head_row[b] : b;
     row_ok = (row >= 0 && row < a.M) ? row : -1;
-    if (row_ok < 0) set_status(MD_DEV_BAD_ROW);
+    if (row_ok < 0 && !idle) set_status(MD_DEV_BAD_ROW);
   }
   __syncthreads();
   if (j >= tp.T) return;
   const int d = tp.depth[j];
   int32_t tok;
-  if (j == 0) {
+  if (idle) {
+    tok = 0;
+  } else if (j == 0) {
     tok = a.root_token[b];
   } else if (row_ok < 0) {
     tok = -1;
@@ -46,7 +50,7 @@ __global__ void __launch_bounds__(MD_MAX_T) tree_build_kernel(const __grid_const
     tok = a.topk_ids[(size_t(row_ok) * a.K + (d - 1)) * a.kmax + tp.rank[j]];
   }
   a.tokens[size_t(b) * tp.T + j] = tok;
-  a.pos[size_t(b) * tp.T + j] = a.prefix_len[b] + d;
+  a.pos[size_t(b) * tp.T + j] = (idle ? 0 : P) + d;
   if (b == 0) {
     a.parent[j] = tp.parent[j];
     for (int w = 0; w < tp.W; ++w) a.anc[size_t(j) * tp.W + w] = tp.anc[j][w];

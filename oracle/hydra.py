@@ -69,6 +69,9 @@ def hydra_draft(parent, head_rank, h_bits, E_bits, W1_bits, b1_bits, Wv_bits, ro
     logits = {}
     for b in range(B):
         row = b if head_row is None else int(head_row[b])
+        if prefix_len[b] == -1:                       # holds no request: as in `tree.tree_build`
+            pos[b] = dep
+            continue
         for j in range(T):
             pos[b, j] = prefix_len[b] + dep[j]
             if j == 0:

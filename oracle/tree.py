@@ -105,7 +105,8 @@ def tree_build(parent, head_rank, topk_ids, root_token, prefix_len, head_row=Non
     """tokens [B, T], parent [T], ancestor words [T, W], positions [B, T].
 
     tokens[b, 0] is the request's root token; a node at depth d with rank r
-    takes ``topk_ids[row_b, d - 1, r]``; row_b is ``head_row[b]`` or b.
+    takes ``topk_ids[row_b, d - 1, r]``; row_b is ``head_row[b]`` or b. A row with
+    prefix -1 holds no request: tokens 0, positions the depths.
     """
     parent = np.asarray(parent)
     B = len(root_token)
@@ -115,6 +116,9 @@ def tree_build(parent, head_rank, topk_ids, root_token, prefix_len, head_row=Non
     pos = np.zeros((B, T), dtype=np.int32)
     for b in range(B):
         row = b if head_row is None else int(head_row[b])
+        if prefix_len[b] == -1:
+            pos[b] = dep
+            continue
         for j in range(T):
             if j == 0:
                 tokens[b, j] = root_token[b]

@@ -210,3 +210,23 @@ def test_70b_hydra_rank0_path_matches_oracle():
             break
         node, node_tok = nxt
     assert checked >= 10
+
+
+def test_idle_rows_of_a_padded_batch():
+    """prefix -1: root -1 and head row -1 are not looked at, and the other rows do not notice."""
+    B, d, V, kph, n = 3, 256, 2048, (4, 3, 2, 2), 16
+    tree = md.Tree(*md.tree_arrays(md.select_tree(kph, TREE_ACCEPT, n)), kph)
+    _, _, depth = ot.spec_from_tuples(ot.select_tree(kph, TREE_ACCEPT, n))
+    h, E, W1, b1, Wv = (bf16_tensor(gen.normal_bf16(3, s, sh, sd)) for s, sh, sd in (
+        ("h", (B, d), 1.0), ("E", (V, d), 1.0), ("W1", (4, d, d), 0.02), ("b1", (4, d), 0.02), ("Wv", (4, d, V), 0.02)))
+    ws = md.workspace(md.hydra_workspace_bytes(tree, B, d, V, 4))
+    got = []
+    md.device_status(clear=True)
+    for root, P, row in (([7, 9, 11], [5, 0, 40], [0, 1, 2]), ([7, -1, 11], [5, -1, 40], [0, -1, 2])):
+        tok, par, anc, pos = _outputs(B, tree.T)
+        md.hydra_draft(tree, h, E, W1, b1, Wv, i32(root), i32(P), tok, par, anc, pos, ws, head_row=i32(row))
+        assert md.device_status(clear=True) == 0
+        got.append((tok.cpu().numpy(), pos.cpu().numpy()))
+    (t0, p0), (t1, p1) = got
+    assert not t1[1].any() and p1[1].tolist() == list(depth)
+    assert np.array_equal(t0[[0, 2]], t1[[0, 2]]) and np.array_equal(p0[[0, 2]], p1[[0, 2]])

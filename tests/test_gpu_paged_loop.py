@@ -165,3 +165,61 @@ def test_a_captured_fork_replays_after_larger_ones():
     for got, want in ((step.block_table, table), (step.n_pages, cnt), (step.refcount, ref), (glen, length)):
         assert np.array_equal(got.cpu().numpy(), want)
     assert all(bool((x == 0x7F).all()) for x in junk)
+
+
+@pytest.mark.parametrize("mode", ["greedy", "typical", "sample", "rejection"])
+def test_padded_batch_feeds_its_own_outputs_back(mode):
+    """Rows that hold no request beside rows that do: root, prefix and head row of each step
+    are the commit's of the step before, untouched by the host, and no status bit is ever set.
+    The target's logits of the idle rows are NaN."""
+    B, d, V, K, kph, n = 4, 256, 2048, 4, (4, 3, 2, 2), 16
+    Hq, Hkv, dh, page, width, pool = 4, 2, 64, 16, 8, 24
+    T = n + 1
+    parent, rank, depth = ot.spec_from_tuples(ot.select_tree(kph, TREE_ACCEPT, n))
+    step = PagedMedusaStep(B=B, M=B * T, d=d, V=V, K=K, k_per_head=kph, tree_tuples=md.select_tree(kph, TREE_ACCEPT, n),
+                           Hq=Hq, Hkv=Hkv, dh=dh, page_size=page, max_pages=width, pool_pages=pool, mode=mode)
+    gW = [bf16_tensor(gen.normal_bf16(0, s, sh, 0.02)) for s, sh in (("W1", (K, d, d)), ("b1", (K, d)), ("Wv", (K, d, V)))]
+    freq = torch.ones(dh // 2, device="cuda")
+    gk = torch.full((1, pool, Hkv, page, dh), float("nan"), dtype=torch.bfloat16, device="cuda")
+    gv = gk.clone()
+    P = np.array([20, -1, 5, -1], dtype=np.int32)
+    gP, root, head_row = i32(P), i32([3, -1, 1000, -1]), i32([0, -1, 2 * T, -1])
+    rng = np.random.default_rng(1)
+    md.device_status(clear=True)
+    step.prefill_pages(gP)
+    gk[:, step.block_table[[0, 2]][step.block_table[[0, 2]] >= 0].long()] = 0
+    gv.copy_(gk)
+    hosts = root.cpu().numpy(), head_row.cpu().numpy()
+    for s in range(4):
+        if s == 2:                                        # row 2's request ends
+            P[2] = -1
+            gP.copy_(i32(P))
+            step.prefill_pages(gP)
+        live = [b for b in range(B) if P[b] >= 0]
+        h = gen.normal_bf16(10 + s, "h", (B * T, d), 1.0)
+        if mode == "rejection":
+            step.u_draft.copy_(torch.rand(step.u_draft.shape, generator=torch.Generator().manual_seed(s)))
+        step.heads(bf16_tensor(h), *gW)
+        step.build(root, gP, head_row=head_row)
+        rtok, _, _, rpos = ot.tree_build(parent, rank, step.topk_ids.cpu().numpy(), hosts[0], P, head_row=hosts[1])
+        assert np.array_equal(step.tokens.cpu().numpy(), rtok) and np.array_equal(step.pos.cpu().numpy(), rpos)
+        assert (rtok >= 0).all() and (rtok < V).all() and (rpos >= 0).all()
+        step.reserve(gP)
+        qkv = bf16_tensor(gen.normal_bf16(s, "q", (B, T, Hq + 2 * Hkv, dh), 1.0))
+        step.append(*qkv.split([Hq, Hkv, Hkv], dim=2), step.pos, freq, gk[0], gv[0], gP)
+        step.attention(step.q, gk[0], gv[0], gP)
+        idle = [b for b in range(B) if P[b] < 0]
+        assert not step.attn_out[idle].any() and torch.isfinite(step.attn_out).all()
+        logits = synth.planted_logits(20 + s, parent, rtok, V, TREE_ACCEPT)
+        logits[idle] = np.nan
+        step.accept(f32(logits))
+        step.commit(gk, gv, gP)
+        step.trim()
+        L, new = step.accept_len.cpu().numpy(), step.new_prefix_len.cpu().numpy()
+        assert md.device_status() == 0
+        assert (new[live] == P[live] + L[live] + 1).all() and (new[idle] == -1).all()
+        assert step.n_pages.cpu().tolist() == [max(0, -(-int(p) // page)) for p in new]
+        gP.copy_(step.new_prefix_len)
+        root, head_row, P = step.next_root, step.next_head_row, new.copy()
+        hosts = root.cpu().numpy(), head_row.cpu().numpy()
+        assert (hosts[0][idle] == -1).all() and (hosts[1][idle] == -1).all() and (hosts[1][live] >= 0).all()

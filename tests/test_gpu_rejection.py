@@ -175,3 +175,21 @@ def test_rejection_refuses_children_that_skip_a_rank():
     p = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
     with pytest.raises(md.MedusaError, match="unsupported"):
         md.tree_accept_rejection(z, t, tree, torch.zeros((1, 1, 64), device="cuda"), u, u, o, p, o)
+
+
+def test_head_row_of_an_idle_row_is_no_error():
+    """-1 (a commit's of an idle or refused request) accepts nothing and sets no bit; other rows outside [0, M) set one."""
+    parent, rank, V = [-1, 0], [0, 0], 64
+    rng = np.random.default_rng(6)
+    hl = rng.standard_normal((2, 1, V)).astype(np.float32)
+    tl = np.full((3, 2, V), -50.0, dtype=np.float32)
+    tl[:, 0, 9] = tl[:, 1, 30] = 50.0                     # the target wants 9, then 30
+    tokens = np.array([[5, 9], [0, 0], [5, 9]], dtype=np.int32)
+    half = np.full((3, 2), 0.5, dtype=np.float32)
+    for bad, status in ((-1, 0), (2, md.binding.DEV_BAD_ROW), (-2, md.binding.DEV_BAD_ROW)):
+        md.device_status(clear=True)
+        acc, path, bonus = (torch.full(sh, -9, dtype=torch.int32, device="cuda") for sh in ((3,), (3, 2), (3,)))
+        md.tree_accept_rejection(f32(tl), i32(tokens), md.Tree(parent, rank, [16]), f32(hl), f32(half), f32(half), acc, path,
+                                 bonus, temperature=1.0, temperature_q=1.0, head_row=i32([0, bad, 1]))
+        assert md.device_status(clear=True) == status
+        assert acc.tolist() == [1, 0, 1] and bonus.tolist() == [30, 9, 30] and path.tolist() == [[0, 1], [0, -1], [0, 1]]

@@ -92,3 +92,12 @@ def test_tree_build_tokens_decode_to_head_and_rank():
             assert t % 100 == tups[j - 1][-1]
         assert list(pos[b] - P[b]) == list(depth)
     assert list(par) == list(parent)
+
+
+def test_idle_row_has_tokens_and_positions_in_range():
+    """prefix -1: neither the root nor the head row is looked at."""
+    parent, rank, depth = ot.spec_from_tuples(ot.select_tree((4, 3, 2, 2), TREE_ACCEPT, 16))
+    ids = np.arange(1, 2 * 4 * 4 + 1).reshape(2, 4, 4)
+    tokens, _, _, pos = ot.tree_build(parent, rank, ids, [7, -1], [3, -1], head_row=[1, -1])
+    assert not tokens[1].any() and pos[1].tolist() == list(depth)
+    assert tokens[0].all() and (pos[0] - 3).tolist() == list(depth)
