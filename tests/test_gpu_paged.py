@@ -730,3 +730,61 @@ def test_scores_far_apart_and_rows_of_nan():
         wide = 2.0 ** -7
         tol = 2 * (wide + 2.0 ** -8) * absv + 2.0 ** -8 * np.abs(ref)
         assert (np.abs(got - ref) <= tol)[~want].all()
+
+
+def _climbing(rng, slots):
+    """Levels of the slots, one for 64 of them: rising by up to 12 a step to at most 60, then from 0 again.
+    The steps lie on both sides of 8, where a running reference maximum moves."""
+    out, level = [], 0.0
+    for i in range(-(-slots // 64)):
+        if i and rng.random() < 0.06:
+            level = 0.0
+        out += [level] * 64
+        level = min(level + rng.choice([0.0, 4.0, 7.75, 8.25, 9.0, 12.0]), 60.0)
+    return np.array(out[:slots])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,dh,page,P", [(1, 1, 4, 1, 128, 64, (20001, 20001)),     # one tile, cut over a cluster
+                                                  (80, 1, 8, 2, 64, 16, (500, 1180)),        # one tile, whole
+                                                  (20, 40, 16, 4, 128, 64, (900, 1950)),     # two tiles
+                                                  (400, 5, 4, 1, 64, 16, (200, 590))],       # half a CTA's form
+                         ids=["cluster", "one-tile", "two-tiles", "short"])
+def test_maxima_that_climb_along_a_walk(B, T, Hq, Hkv, dh, page, P, dtype):
+    """Walks of 8 to 20 jobs of 64 keys whose scores climb: sums and results are rescaled on the way,
+    inside and between stretches of 128 keys. A key's weight is about 2^level and its value about
+    2^-level, so that every step of the climb counts alike: a rescaling left out or done twice is
+    off by the result's size.
+
+    Tolerance: scores of up to 62 in log2 units, sums of dh products in fp32, each off by at most
+    dh 2^-24 of that, so a weight by ln 2 times 62 dh 2^-24; numerator and denominator twice that of A.
+    bf16 results: the weights' and the result's rounding, 2^-8 each, on top."""
+    rng = np.random.default_rng(B + T)
+    parent, rank = _tree(T - 1)
+    lens = [int(x) for x in rng.integers(P[0], P[1] + 1, B)]
+    table, pool = _table(rng, lens, T, page)
+    q = bf16_to_f64(gen.normal_bf16(31, "q", (B, T, Hq, dh), 0.25))
+    k = bf16_to_f64(gen.normal_bf16(31, "k_cache", (pool, Hkv, page, dh), 0.25))
+    v = bf16_to_f64(gen.normal_bf16(31, "v_cache", (pool, Hkv, page, dh), 1.0))
+    q[..., 0] = np.resize([1.0, 0.75, 0.5], Hq)
+    for b, p in enumerate(lens):
+        level = _climbing(rng, p + T)
+        level[p:] = level[p - 1]                              # the tree's nodes: the last level
+        for i in range(-(-(p + T) // page)):
+            at = level[i * page:(i + 1) * page]
+            k[table[b, i], :, :len(at), 0] = at
+            v[table[b, i], :, :len(at)] *= (2.0 ** -at)[None, :, None]
+    bits = [to_bits(torch.from_numpy(x).to(torch.bfloat16)) for x in (q, k, v)]
+    scale = float(np.float32(np.log(2.0)))
+    md.device_status(clear=True)
+    out = _attention(*(bf16_tensor(x) for x in bits), i32(table), i32(lens), parent, rank, dtype, scale=scale)
+    assert md.device_status() == 0
+    ref = op.tree_attention_paged(*bits, table, lens, parent, scale)
+    absv = op.tree_attention_paged(bits[0], bits[1], bits[2] & 0x7FFF, table, lens, parent, scale)
+    off = 2 * np.log(2.0) * 62 * dh * 2.0 ** -24
+    tol = off * absv
+    if dtype == torch.bfloat16:
+        tol = (off + 2 * 2.0 ** -8) * absv + 2.0 ** -8 * np.abs(ref)
+    got = out.float().cpu().numpy().astype(np.float64)
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), (bad.mean(), np.argwhere(bad)[:3], got[bad][:3], ref[bad][:3], tol[bad][:3])
