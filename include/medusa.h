@@ -539,10 +539,13 @@ MD_API md_status md_attention_paged_workspace(int32_t B, int32_t T, int32_t Hq, 
  *         MD_DEV_BAD_PREFIX and writes zeros for that request. A bad page is
  *         read as zeros.
  * scale   softmax scale; 0 means 1/sqrt(dh).
- * out     [B, T, Hq, dh] fp32 (MD_OUT_F32; weights kept to 24 bits, sums of at most
- *         128 keys in the tensor cores: off by less than 1e-6 of the result) or bf16
- *         (MD_OUT_BF16; weights rounded to bf16, about twice as fast over long
- *         prefixes).
+ * out     [B, T, Hq, dh], whose type also decides the weights' bits. fp32
+ *         (MD_OUT_F32): weights of 24 bits, sums of at most 128 keys in the tensor
+ *         cores. Measured from 128 to 660000 slots, 2-norm of the error over the
+ *         result's: 8e-7 with N(0, 1) inputs, 2.3e-6 with values of one sign (what the
+ *         tensor cores drop adds up); scores of up to 40 put single elements 5e-6 of
+ *         sum w |v| off. bf16 (MD_OUT_BF16): weights rounded to bf16, 0.0023 where the
+ *         result's own rounding is 0.0017, and up to twice as fast.
  * q, k_pages, v_pages and out 16-byte aligned; out not q. The workspace is
  * md_attention_paged_workspace()'s, 256-byte aligned, with any contents.
  * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_WORKSPACE, MD_ERR_CUDA. */

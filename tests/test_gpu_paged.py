@@ -788,3 +788,42 @@ def test_maxima_that_climb_along_a_walk(B, T, Hq, Hkv, dh, page, P, dtype):
     got = out.float().cpu().numpy().astype(np.float64)
     bad = ~(np.abs(got - ref) <= tol)
     assert not bad.any(), (bad.mean(), np.argwhere(bad)[:3], got[bad][:3], ref[bad][:3], tol[bad][:3])
+
+
+@pytest.mark.parametrize("positive", [False, True], ids=["values-of-both-signs", "values-of-one-sign"])
+@pytest.mark.parametrize("T,P", [(1, 660_000), (65, 330_000), (17, 128)], ids=["one-tile", "two-tiles", "short"])
+def test_fp32_results_keep_their_bits_at_any_length(T, P, positive):
+    """fp32 results of over 20000 keys a stream against 64 bits, N(0, 1) inputs.
+
+    Bounds. A score: dh / 16 = 4 steps of the tensor cores' sum, each dropping less than 2^-23 of a
+    partial sum of at most 6 (in units of the scaled score): a weight is off by at most 2.9e-6, and its
+    exponential by 2^-22 more. With values of both signs the weights' errors and the result are sums
+    of the same random signs: 3.2e-6 of the result in the 2-norm (weights of two bf16 parts alone would
+    give 2^-16 / sqrt(3) = 8.8e-6). With values of one sign what the accumulator drops adds up: 8 steps
+    and 3 parts in a stretch of 128 keys, below 24 * 2^-23 = 2.9e-6, with the weights 6.1e-6 of A."""
+    parent, rank = _tree(T - 1)
+    Hq, dh, page = 4, 64, 64
+    n = -(-(P + T) // page)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    kp, vp = (torch.randn((n, 1, page, dh), generator=g, device="cuda").bfloat16() for _ in range(2))
+    vp = vp.abs() if positive else vp
+    q = torch.randn((1, T, Hq, dh), generator=g, device="cuda").bfloat16()
+    table = torch.randperm(n, generator=g, device="cuda").to(torch.int32)[None].contiguous()
+    md.device_status(clear=True)
+    out = _attention(q, kp, vp, table, i32([P]), parent, rank, torch.float32)
+    assert md.device_status() == 0
+    k, v = (x[table[0].long(), 0].reshape(-1, dh)[:P + T].double() for x in (kp, vp))
+    hide = torch.ones((T, T), dtype=torch.bool)
+    for t in range(T):
+        hide[t, list(_ancestors(parent, t))] = False
+    err = size = 0.0
+    for h in range(Hq):
+        x = q[0, :, h].double() @ k.T / dh ** 0.5
+        x[:, P:].masked_fill_(hide.cuda(), float("-inf"))
+        w = torch.softmax(x, dim=1)
+        ref = w @ v
+        off = (out[0, :, h].double() - ref).abs()
+        assert (off <= 6.1e-6 * (w @ v.abs())).all(), float((off / (w @ v.abs())).max())
+        err, size = err + float(off.square().sum()), size + float(ref.square().sum())
+    if not positive:
+        assert (err / size) ** 0.5 <= 3.2e-6, (err / size) ** 0.5
