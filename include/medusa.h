@@ -545,7 +545,8 @@ MD_API md_status md_attention_paged_workspace(int32_t B, int32_t T, int32_t Hq, 
  *         result's: 8e-7 with N(0, 1) inputs, 2.3e-6 with values of one sign (what the
  *         tensor cores drop adds up); scores of up to 40 put single elements 5e-6 of
  *         sum w |v| off. bf16 (MD_OUT_BF16): weights rounded to bf16, 0.0023 where the
- *         result's own rounding is 0.0017, and up to twice as fast.
+ *         result's own rounding is 0.0017, and over long prefixes less than half the
+ *         time. An infinite V that a row sees makes that element infinite or NaN.
  * q, k_pages, v_pages and out 16-byte aligned; out not q. The workspace is
  * md_attention_paged_workspace()'s, 256-byte aligned, with any contents.
  * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_WORKSPACE, MD_ERR_CUDA. */
