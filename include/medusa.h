@@ -86,7 +86,8 @@ enum {
  *   attention: dh in {64, 128}, Hq % Hkv == 0, Hq / Hkv <= 16.
  *   paged:     as attention; page_size % 16 == 0 for md_tree_attention_paged,
  *              any page_size >= 1 for the other calls; B <= 65535; max_pages *
- *              page_size, B * max_pages and pool_pages * Hkv within int32.
+ *              page_size, B * max_pages and pool_pages * Hkv within int32; for
+ *              md_pages_fork layers * Hkv and page_size * dh / 8 as well.
  */
 #define MD_MAX_T 128
 #define MD_MAX_K 8

@@ -1770,7 +1770,10 @@ md_status md_pages_fork(md_bf16* k_pages, md_bf16* v_pages, int32_t layers, int3
   if (s != MD_OK) return s;
   if (layers < 1) return MD_ERR_INVALID_ARG;
   if ((s = paged_check(B, pool_pages, page_size, max_pages, Hkv, dh)) != MD_OK) return s;
-  if (int64_t(layers) * Hkv > INT32_MAX - md::pages::kCopyHeads) return MD_ERR_UNSUPPORTED;
+  // the copy counts layers' heads, and a head's 16-byte pieces of a page, in 32 bits
+  if (int64_t(layers) * Hkv > INT32_MAX - md::pages::kCopyHeads ||
+      int64_t(page_size) * (dh / 8) > INT32_MAX - md::pages::kCopyLoads * md::pages::kCopyThreads)
+    return MD_ERR_UNSUPPORTED;
   if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(refcount, 16)) return MD_ERR_INVALID_ARG;
   if (!ws || ws_bytes < need || !aligned(ws, 256)) return MD_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -176,3 +176,14 @@ def test_fork_workspace_stays_where_it_is(monkeypatch):
     for n in (1, 16, 17, 1, 1024):
         step.fork(pool, pool, i32(n), i32(n), i32(B))
     assert len(set(seen)) == 1
+
+
+def test_fork_refuses_pages_it_cannot_count():
+    """Of a page of 2^27 slots of 128 the copy's 32-bit count of 16-byte pieces would overflow."""
+    p = 1 << 20
+
+    def fork(page_size, d):
+        return md.lib().md_pages_fork(p, p, 1, 2, 1, page_size, d, p, p, p, p, 2, 1, p, p, 1, None, 0, None)
+
+    assert fork(1 << 27, 128) == -2 and fork((1 << 27) - 1, 128) == -2 and fork(1 << 28, 64) == -2
+    assert fork((1 << 27) - 65, 128) == -4 and fork(1 << 27, 64) == -4      # taken, but for the missing workspace
