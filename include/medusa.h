@@ -524,6 +524,8 @@ MD_API md_status md_tree_commit(md_bf16* k_cache, md_bf16* v_cache, int32_t S_ma
 /* Output types of md_tree_attention_paged. */
 enum { MD_OUT_F32 = 0, MD_OUT_BF16 = 1 };
 
+/* Workspace bytes md_tree_attention_paged asks for. The present kernel joins its
+ * partial results in shared memory and leaves the workspace untouched. */
 MD_API md_status md_attention_paged_workspace(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t dh,
                                               int32_t page_size, int32_t max_pages, size_t* bytes);
 
@@ -548,6 +550,9 @@ MD_API md_status md_attention_paged_workspace(int32_t B, int32_t T, int32_t Hq, 
  *         sum w |v| off. bf16 (MD_OUT_BF16): weights rounded to bf16, 0.0023 where the
  *         result's own rounding is 0.0017, and over long prefixes less than half the
  *         time. An infinite V that a row sees makes that element infinite or NaN.
+ * The work is laid out by what the table can hold (max_pages * page_size), so a
+ * table much wider than the sequences costs time: many requests of a few hundred
+ * slots up to twice as much from a width of 2048 on, trees of a batch from 65536 on.
  * q, k_pages, v_pages and out 16-byte aligned; out not q. The workspace is
  * md_attention_paged_workspace()'s, 256-byte aligned, with any contents.
  * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_WORKSPACE, MD_ERR_CUDA. */

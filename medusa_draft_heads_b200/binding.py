@@ -499,7 +499,9 @@ def attention_paged_workspace_bytes(B, T, Hq, Hkv, dh, page_size, max_pages) -> 
 
 def tree_attention_paged(q, k_pages, v_pages, block_table, prefix_len, tree: Tree, out, ws, scale=0.0, stream=None):
     """md_tree_attention_paged: q [B,T,Hq,dh], pools [pages,Hkv,page_size,dh] bf16, block_table
-    [B,max_pages] int32 -> out [B,T,Hq,dh], fp32 or bf16 (by its dtype). prefix_len -1: an idle slot."""
+    [B,max_pages] int32 -> out [B,T,Hq,dh]. out's dtype also decides the bits of the softmax weights
+    in the product with V: float32 24 (and about twice the time over long prefixes), bfloat16 8.
+    prefix_len -1: an idle row."""
     what = "tree_attention_paged"
     B, T, Hq, dh = _dims(what, q, "q", 4)
     pages, Hkv, page, _ = _dims(what, k_pages, "k_pages", 4)

@@ -31,9 +31,11 @@
 //               exp2(S - m); sums in fp32.
 //
 // P is rounded to bf16 for the product with V where the result is bf16: a weight's
-// error, at most 2^-8 of it either way, averages out over the keys, and the result is
-// rounded to the same precision (0.0023 of the result against 64 bits, 0.0017 being
-// the last rounding's own). For fp32 results P is three bf16 parts, 24 bits, and P V
+// error, at most 2^-8 of it either way, averages out over the keys as V does, and the
+// result is rounded to the same precision (0.0023 of the result against 64 bits,
+// 0.0017 being the last rounding's own: two roundings of one size). A second part of P
+// leaves 0.0017 and was not worth its product: 70B batch of 8 125 us against 103, 70B
+// tree 27 against 22.6. For fp32 results P is three bf16 parts, 24 bits, and P V
 // three products; S then has one buffer, the parts needing the other's columns. The
 // tensor cores' accumulator drops what it cannot hold at every step (8e-6 of the result
 // over 20000 keys), so after every 128 keys O is added to a sum in local memory:
@@ -43,8 +45,8 @@
 // The KV splits of a unit are the CTAs of a cluster: O and (m, sum) of every
 // stream are staged in shared memory, and each CTA combines its share of the
 // rows from all of them (distributed shared memory). Splits are made of the
-// request's own length on the device, so a table wider than the sequences costs
-// little.
+// request's own length on the device, so that none is empty in a wide table; how many
+// there are, and the CTAs' shape, go by the table's width (paged_attn_plan).
 //
 // Slots behind the tree's last hold anything, NaN included: their scores are
 // replaced, and their V rows zeroed in shared memory (0 * NaN would reach O). A
@@ -53,7 +55,8 @@
 // results at the end.
 //
 // What bounds it. Long prefixes with few rows: bytes (16 requests of 20k to 33k
-// slots, one node: 266 us, 6.3 TB/s, 97 % of a copy's rate). Many rows: the two-tile
+// slots, one node: 264 us, 6.4 TB/s, 97 % of a copy's rate, replayed from a cool start;
+// call after call the power cap takes the clocks to 1.6 GHz, 310 us, 83 %). Many rows: the two-tile
 // walk takes 1.76 us a chunk of 128 keys where its tensor work takes 1.34 (measured
 // without the softmax: S with N = 64 is held back by shared memory, 43 clocks an MMA
 // against 32) and the special-function unit 1.08; 70B batch of 8: 103 us, 0.66

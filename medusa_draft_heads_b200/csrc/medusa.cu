@@ -944,7 +944,10 @@ struct PagedAttnPlan {
 // past one wave fill the SMs as they come, with half a CTA's time left uneven; and
 // no call is faster than its keys' bytes from memory, 1.1 times that in one wave (a
 // batch's lengths differ, and its longest request then keeps one CTA). Chunks are
-// counted by what the table can hold: the lengths are on the device.
+// counted by what the table can hold: the lengths are on the device. In a table much
+// wider than the sequences the bytes' time hides the shapes' differences, and the first
+// one stands: 32 requests of 500 slots take 13.5 us in a tight table and 26 from 2048
+// slots on, the 70B batch of 8 over 4000 slots 111 us up to 32768 and 257 at 131072.
 //   70B tree, B = 1 (40 tiles, 33 chunks): one tile, 3 splits 23.7 us; two tiles, 5
 //     splits 26.7. B = 8: one tile 124, two tiles 113.6.
 //   Decoding, 8 KV heads, 4096 slots: 1 split 32.9, 4 15.3, 8 12.5, 12 (two waves)

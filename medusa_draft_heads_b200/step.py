@@ -134,6 +134,12 @@ class PagedMedusaStep(MedusaStep):
         step.attention(step.q, k_pages[i], v_pages[i], prefix_len)
         step.accept(logits); step.commit(k_pages, v_pages, prefix_len)                       # all layers at once
         step.trim()                                    # pages past the new prefixes go back
+        prefix_len.copy_(step.new_prefix_len)          # and step.next_root, step.next_head_row as they are
+
+    A row whose commit was refused (next_head_row -1 where prefix_len is not: it had no
+    pages, or its path was none) keeps its prefix; its root token is still tokens[b, 0].
+    out_dtype: of the attention's results; bfloat16 halves its time over long prefixes
+    and takes 8 bits of the softmax weights instead of 24.
     """
 
     def __init__(self, *, page_size, max_pages, pool_pages, out_dtype=torch.float32, **kw):
