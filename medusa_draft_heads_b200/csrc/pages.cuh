@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(ForkArgs a) {
   __shared__ int s_src[kMaxForks], s_dst[kMaxForks], s_fresh[kMaxForks], s_owner[kMaxForks];
   __shared__ int part[kWarps];
   const int i = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int src = -1, dst = -1, len = -1;
+  int src = -1, dst = -1, len = -1, last_page = -1;
   if (i < a.n) {
     src = a.src[i];
     dst = a.dst[i];
@@ -269,6 +269,10 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(ForkArgs a) {
         const int hs = a.n_pages[src], hd = a.n_pages[dst];
         if (hs < 0 || hs > a.max_pages || hd < 0 || hd > a.max_pages) bad = MD_DEV_BAD_PAGE;
         else if (len > (long long)hs * a.page) bad = MD_DEV_BAD_PREFIX;
+        if (!bad && len > 0 && len % a.page > 0) {   // the page to be copied
+          last_page = a.table[size_t(src) * a.max_pages + len / a.page];
+          if (last_page < 0 || last_page >= a.pool) bad = MD_DEV_BAD_PAGE;
+        }
       }
     }
     if (bad) {
@@ -307,13 +311,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(ForkArgs a) {
   __shared__ int s_full[kMaxForks];
   s_full[i] = empty ? -1 : full;
   if (i < a.n) {
-    ForkJob job = {0, 0, 0, 0};
-    if (!empty && rows > 0) {
-      const int from = a.table[size_t(src) * a.max_pages + full];
-      if (from < 0 || from >= a.pool) set_status(MD_DEV_BAD_PAGE);
-      else job = {from, s_fresh[i], rows, 0};
-    }
-    a.jobs[i] = job;
+    a.jobs[i] = !empty && rows > 0 ? ForkJob{last_page, s_fresh[i], rows, 0} : ForkJob{0, 0, 0, 0};
   }
   __syncthreads();
   for (int f = warp; f < a.n; f += kWarps) {

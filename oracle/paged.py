@@ -138,6 +138,9 @@ def pages_fork(k_pages, v_pages, table, n_pages, refcount, src, dst, length):
     page = k.shape[3]
     jobs = []
     for i in range(len(src)):
+        n = int(length[src[i]]) if src[i] != -1 else -1
+        if n > 0 and n % page and not 0 <= table[src[i], n // page] < len(ref):
+            continue                                    # no page to copy from
         if src[i] != -1 and dst[i] not in [s for s in src if s != -1] and dst[i] not in [d for _, d in jobs]:
             jobs.append((int(src[i]), int(dst[i])))
     for _, d in jobs:

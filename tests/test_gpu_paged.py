@@ -597,6 +597,26 @@ def test_fork_leaves_out_what_cannot_be():
     assert g[4].cpu().tolist() == [1, 1, 1, 1, 1, 1]
 
 
+@pytest.mark.parametrize("bad", [-1, 6, -2 ** 31])
+def test_fork_is_left_out_without_a_page_to_copy(bad):
+    """The source ends inside a page outside the pool: the destination stays as it is, and no page is taken."""
+    page, pool = 16, 6
+    table = np.array([[0, bad], [2, -1], [3, bad], [-1, -1], [-1, -1]], dtype=np.int32)
+    cnt, ref = np.array([2, 1, 2, 0, 0], dtype=np.int32), np.array([1, 0, 1, 1, 0, 0], dtype=np.int32)
+    length = np.array([20, 9, 32, -1, -1], dtype=np.int32)             # row 2 ends with its pages: nothing to copy
+    k = gen.normal_bf16(1, "k_cache", (1, pool, 1, page, 64), 1.0)
+    src, dst = np.array([0, 1]), np.array([3, 4])
+    g = [bf16_tensor(k), bf16_tensor(k)] + [i32(x) for x in (table, cnt, ref, length)]
+    md.device_status(clear=True)
+    md.pages_fork(g[0], g[1], g[2], g[3], g[4], i32(src), i32(dst), g[5], md.workspace(4096))
+    assert md.device_status(clear=True) == md.binding.DEV_BAD_PAGE
+    k2, _, t2, c2, r2, l2 = op.pages_fork(k, k, table, cnt, ref, src, dst, length)
+    assert t2[3].tolist() == [-1, -1] and t2[4].tolist() == [1, -1] and r2.tolist() == [1, 1, 1, 1, 0, 0]
+    assert np.array_equal(to_bits(g[0]), k2) and np.array_equal(to_bits(g[1]), k2)
+    for got, want in zip(g[2:], (t2, c2, r2, l2)):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_two_streams_with_workspaces_of_their_own():
     """Attention calls of two streams at once, and one call's result on a side stream."""
     rng = np.random.default_rng(21)
