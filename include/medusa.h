@@ -620,7 +620,8 @@ MD_API md_status md_tree_commit_paged(md_bf16* k_pages, md_bf16* v_pages, int32_
  * block_table [B, max_pages], n_pages [B] (pages a row holds), refcount
  * [pool_pages] (rows that hold a page; 0 = free) int32; 16-byte aligned
  * refcount. extra >= 0. A row is served if its need and those of the rows
- * before it fit the free pages; the others keep what they hold and
+ * before it fit the free pages; the others keep what they hold (n_pages tells
+ * which; a prompt must not be taken as written without its pages) and
  * MD_DEV_NO_PAGES is set. A row whose wanted pages exceed max_pages
  * (MD_DEV_BAD_PREFIX) or whose n_pages is not in [0, max_pages]
  * (MD_DEV_BAD_PAGE) is left alone. length = -1 frees a row. B <= 16384.
