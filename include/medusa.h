@@ -645,7 +645,8 @@ MD_API md_status md_pages_fork_workspace(int32_t B, int32_t n, size_t* bytes);
  * length [B] int32: length[dst] = length[src] (updated in place; a negative
  * length empties dst). length[src] > n_pages[src] * page_size
  * (MD_DEV_BAD_PREFIX), an impossible n_pages or a bad page where the copy would
- * come from (MD_DEV_BAD_PAGE) leaves the fork out. Without a free page (MD_DEV_NO_PAGES) dst ends empty, length -1.
+ * come from (MD_DEV_BAD_PAGE) leaves the fork out. Without a free page
+ * (MD_DEV_NO_PAGES) dst ends empty, length -1.
  * k_pages, v_pages [layers, pool_pages, Hkv, page_size, dh] bf16; the table
  * arrays as in md_pages_resize. Workspace 256-byte aligned, any contents.
  * Errors: MD_ERR_INVALID_ARG, MD_ERR_UNSUPPORTED, MD_ERR_WORKSPACE, MD_ERR_CUDA. */
